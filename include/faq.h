@@ -60,7 +60,7 @@ typedef enum {
   FA_ERR_CUDA = 5,            /* a CUDA runtime call or launch failed       */
   FA_ERR_TIMEOUT = 6,         /* a kernel's bounded wait ran out            */
   FA_ERR_WORKSPACE = 7,       /* workspace missing or too small             */
-  FA_ERR_BOUNDS = 8           /* FA_DEBUG_BOUNDS build: an index check failed */
+  FA_ERR_BOUNDS = 8           /* a kernel's index check failed (fa_check_device_status) */
 } fa_status;
 
 typedef enum { FA_LAYOUT_BNSD = 0, FA_LAYOUT_BSND = 1 } fa_layout;
@@ -329,10 +329,168 @@ FAQ_API size_t fa_attention_workspace_size(const fa_qtensor* q, const fa_qtensor
 FAQ_API size_t fa_attention_workspace_size_qkv(const fa_qtensor* q, const fa_qtensor* k, const fa_qtensor* v,
                                                int num_splits);
 
+/* ---------------------------------------------------------- paged caches ---
+ * Serving operators on a K/V cache kept in pages: rotary positions with the
+ * quantized append, attention of a ragged batch of new tokens over the cache,
+ * the attention weight each cached token gathers, and eviction by it.
+ *
+ * Sequence b of a batch has n_b = seq_lens[b] cached tokens; its m_b =
+ * cu_q[b + 1] - cu_q[b] new tokens are the last of them (new token i sits at
+ * cache index n_b - m_b + i).  Cache index j of sequence b is slot
+ * j % page_size of page page_table[b][j / page_size].
+ *
+ * What the host cannot see without a copy (lengths, pages, positions) the
+ * kernels check: a sequence whose length is negative or more than its table
+ * holds, whose cu_q entries do not ascend inside [0, T] or give it more than
+ * max_q new tokens, is left out; an access through a page that is not in
+ * [0, pages), or a rotary position outside the table, is skipped.  Each is
+ * recorded in the device status word (fa_check_device_status ->
+ * FA_ERR_BOUNDS); the call's outputs are then not valid. */
+
+/* Pages of quantized K and V.  mode: FA_MODE_INT8_PER_HEAD,
+ * FA_MODE_FP8_PER_HEAD (scales fp32 [H]), FA_MODE_INT8_PER_TOKEN or
+ * FA_MODE_FP8_PER_TOKEN (scales fp32 [pages, H, page_size] in either layout);
+ * others -> FA_ERR_UNSUPPORTED (a scale over several tokens, or packed codes,
+ * would have to be requantized by an append).
+ * codes: one byte each, [pages, H, page_size, D] (BNSD) or
+ * [pages, page_size, H, D] (BSND), 16-byte aligned.  D: 64 or 128.
+ * page_size: a power of two from 16 to 1024. */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  fa_mode mode;
+  int pages, H, page_size, D;
+  fa_layout layout;
+} fa_paged_cache;
+
+/* The sequences of one call.  page_table: device int32 [B, max_pages], entries
+ * past a sequence's last page are not read.  seq_lens: device int32 [B].
+ * cu_q: device int32 [B + 1], rising from 0; NULL: one new token per sequence
+ * (T == B).  max_q: the largest m_b, or any bound on it (0: T). */
+typedef struct {
+  const int* page_table;
+  const int* seq_lens;
+  const int* cu_q;
+  int B, max_pages, max_q;
+} fa_paged_batch;
+
+/* Rows of new tokens: bf16 [T, H, D], heads and elements dense, `stride`
+ * elements (a multiple of 8, at least H * D) from token to token -- so the q,
+ * k and v columns of one fused projection can be passed as they are.  Rows at
+ * and past cu_q[B] belong to no sequence (a padded batch): they are not read,
+ * and what they would give is left as it was. */
+typedef struct {
+  void* data; /* device, bf16, 16-byte aligned */
+  int T, H, D;
+  long long stride;
+} fa_rows;
+
+/*
+ * fa_rope_table -- cos and sin of every position's rotation angles.
+ *   table: device fp32 [positions, rotary_dim]: entry (p, i) is
+ *   factor * cos(p * inv_freq[i]) for i < rotary_dim / 2, then the sines.
+ *   inv_freq: HOST doubles, rotary_dim / 2 of them (frequencies scaled for
+ *   long contexts are the caller's; the Python binding has the usual rules).
+ *   Angles, cosines and sines are computed in 64 bits and rounded once.
+ *   rotary_dim: even, 2..128.
+ */
+FAQ_API fa_status fa_rope_table(float* table, int positions, int rotary_dim, const double* inv_freq, double factor,
+                                fa_stream_t s);
+
+/*
+ * fa_rope_append -- rotate the new tokens' Q and K by their positions, and
+ * quantize K and V into the cache.
+ *   The first rotary_dim elements of each Q and K head are rotated in pairs
+ *   (2i, 2i+1) (interleaved != 0) or (i, i + rotary_dim / 2):
+ *   a' = a cos - b sin, b' = b cos + a sin with cos, sin = cos_sin[p]; each
+ *   product and each sum is rounded to fp32, the result to bf16.  V is not
+ *   rotated.  p = positions[t] (device int32 [T]), or the token's cache index
+ *   when positions is NULL.  cos_sin: device fp32 [table_positions,
+ *   rotary_dim] as fa_rope_table lays it out, 16-byte aligned; rotary_dim: a
+ *   multiple of 16 up to D, or 0 for no rotation (cos_sin ignored).
+ *   K (rotated, bf16) and V are quantized as fa_quantize does in the cache's
+ *   mode and stored at the tokens' cache indices; in the per-token modes a
+ *   row holding a NaN gets a NaN scale and zero codes.  The per-head modes
+ *   need amax_k, amax_v (device fp32 [H], FA_ERR_NO_CALIBRATION if NULL) and
+ *   (re)write the cache's scales with amax / 127 or amax / 448.
+ *   q, q_out: rows of one T, H and D; q_out may be q (in place).  Both NULL:
+ *   K and V only.  A page written by this call must not be another
+ *   sequence's page too.
+ */
+FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_paged_cache* cache,
+                                 const fa_paged_batch* batch, const float* cos_sin, int table_positions,
+                                 int rotary_dim, const int* positions, int interleaved, const float* amax_k,
+                                 const float* amax_v, const fa_rows* q_out, fa_stream_t s);
+
+/*
+ * fa_paged_attention -- attention of the new tokens over the cache:
+ *   O_i = sum_j softmax_j(softmax_scale * q_i . (s_k k_j)) s_v v_j.
+ *   q: bf16 rows, not quantized; q->H % cache->H == 0 (query head h reads kv
+ *   head h / (Hq / Hkv)).  causal != 0: new token i of sequence b sees cache
+ *   indices j <= n_b - m_b + i; 0: all n_b (cross attention to states kept in
+ *   pages).  softmax_scale <= 0 means 1/sqrt(D).  A row that sees no key has
+ *   output 0 and lse -inf.
+ *   out: device bf16 [T, Hq, D], 16-byte aligned.  lse: nullable device fp32
+ *   [T, Hq], natural-log sum-exp of the scaled scores.
+ *   workspace: fa_paged_attention_workspace_size() bytes, 256-byte aligned
+ *   (FA_ERR_WORKSPACE otherwise); only used during the call's kernels, so
+ *   calls that can overlap (two streams) need one each.
+ *   Scores, maxima, sums and accumulators are fp32; the probabilities enter
+ *   the second product as fp16.
+ */
+FAQ_API fa_status fa_paged_attention(const fa_rows* q, const fa_paged_cache* cache, const fa_paged_batch* batch,
+                                     int causal, float softmax_scale, void* out, float* lse, void* workspace,
+                                     size_t ws_bytes, fa_stream_t s);
+
+/* Workspace bytes of fa_paged_attention for these operands (it does not grow
+ * with the cached lengths).  Returns 0 on invalid arguments. */
+FAQ_API size_t fa_paged_attention_workspace_size(const fa_rows* q, const fa_paged_cache* cache,
+                                                 const fa_paged_batch* batch);
+
+/*
+ * fa_paged_weights -- the attention weight that the new tokens give each
+ * cached token: for sequence b, kv head h and cache index j < n_b
+ *   w = sum over new tokens i that see j and query heads r of h's group of
+ *       exp(softmax_scale * q_ir . (s_k k_j) - lse_ir),
+ *   acc[b][h][j] = w, or acc[b][h][j] + w with accumulate != 0.
+ *   q, causal, softmax_scale as fa_paged_attention's; lse: device fp32
+ *   [T, Hq], what that call returned (rows at -inf give nothing).
+ *   acc: device fp32 [B, Hkv, acc_stride]; acc_stride (tokens) must hold the
+ *   longest sequence (longer ones are left out: FA_ERR_BOUNDS).  Entries at
+ *   and past n_b are left as they were.  Sums are in a fixed order.
+ */
+FAQ_API fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_paged_cache* cache,
+                                   const fa_paged_batch* batch, int causal, float softmax_scale, float* acc,
+                                   long long acc_stride, int accumulate, fa_stream_t s);
+
+/*
+ * fa_paged_evict -- cut every kv head of every sequence to `budget` tokens:
+ * the first `sink`, the last `recent`, and of the rest those of the highest
+ * score (equal scores: the lower index first; NaN below every number).
+ *   scores: device fp32 [B, Hkv, score_stride], score_stride at least the
+ *   longest sequence.  A sequence of at most `budget` tokens keeps them all.
+ *   kept: device int32 [B, Hkv, budget], the kept cache indices ascending,
+ *   then -1.  new_lens: device int32 [B], min(n_b, budget).
+ *   Kept rows (codes, and the per-token modes' scales) move, in order, to
+ *   cache indices 0, 1, ... of the same pages; rows at and past new_lens[b]
+ *   are left as they were, and the pages that only they used are free.
+ *   scores_out: nullable, device fp32 like scores (not the same buffer): the
+ *   kept tokens' scores in order, then 0.  batch->cu_q is not used.  Keys
+ *   keep the rotation of their first positions, so later tokens need explicit
+ *   positions in fa_rope_append.  A page must not be in two sequences.
+ *   budget >= 1, sink + recent <= budget.
+ */
+FAQ_API fa_status fa_paged_evict(const fa_paged_cache* cache, const fa_paged_batch* batch, const float* scores,
+                                 long long score_stride, int budget, int sink, int recent, int* kept, int* new_lens,
+                                 float* scores_out, fa_stream_t s);
+
 /* Synchronise `s`, read and clear this device's status word.  Returns
  * FA_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
- * FA_ERR_BOUNDS if (in a library built with FA_DEBUG_BOUNDS) an index check
- * failed -- the access was skipped, so the outputs are not valid --,
+ * FA_ERR_BOUNDS if an index check failed (the paged operators' checks of
+ * lengths, pages and positions; every other index in a library built with
+ * FA_DEBUG_BOUNDS) -- the access was skipped, so the outputs are not valid --,
  * FA_ERR_CUDA if the stream reports an error, FA_OK otherwise.  The first
  * event since the last check is the one reported. */
 FAQ_API fa_status fa_check_device_status(fa_stream_t s);

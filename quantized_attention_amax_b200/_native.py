@@ -28,6 +28,12 @@ EXPORTS = (
     "fa_attention_decode_noalloc",
     "fa_decode_append",
     "fa_decode_append_workspace_size",
+    "fa_rope_table",
+    "fa_rope_append",
+    "fa_paged_attention",
+    "fa_paged_attention_workspace_size",
+    "fa_paged_weights",
+    "fa_paged_evict",
     "fa_check_device_status",
     "fa_status_str",
     "fa_version",
@@ -48,6 +54,22 @@ class FaQTensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("mode", ctypes.c_int),
                 ("B", ctypes.c_int), ("H", ctypes.c_int), ("S", ctypes.c_int), ("D", ctypes.c_int),
                 ("layout", ctypes.c_int), ("block_tokens", ctypes.c_int)]
+
+
+class FaPagedCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("mode", ctypes.c_int), ("pages", ctypes.c_int), ("H", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("D", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class FaPagedBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("max_pages", ctypes.c_int), ("max_q", ctypes.c_int)]
+
+
+class FaRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("T", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int),
+                ("stride", ctypes.c_longlong)]
 
 
 class FaBranchCfg(ctypes.Structure):
@@ -83,6 +105,17 @@ def lib() -> ctypes.CDLL:
     L.fa_decode_append.restype = I
     L.fa_decode_append_workspace_size.argtypes = [pT, pQ, I, I]
     L.fa_decode_append_workspace_size.restype = S
+    pR, pC, pB = ctypes.POINTER(FaRows), ctypes.POINTER(FaPagedCache), ctypes.POINTER(FaPagedBatch)
+    LL = ctypes.c_longlong
+    L.fa_rope_table.argtypes = [P, I, I, ctypes.POINTER(ctypes.c_double), ctypes.c_double, P]
+    L.fa_rope_append.argtypes = [pR, pR, pR, pC, pB, P, I, I, P, I, P, P, pR, P]
+    L.fa_paged_attention.argtypes = [pR, pC, pB, I, F, P, P, P, S, P]
+    L.fa_paged_attention_workspace_size.argtypes = [pR, pC, pB]
+    L.fa_paged_attention_workspace_size.restype = S
+    L.fa_paged_weights.argtypes = [pR, P, pC, pB, I, F, P, LL, I, P]
+    L.fa_paged_evict.argtypes = [pC, pB, P, LL, I, I, I, P, P, P, P]
+    for name in ("fa_rope_table", "fa_rope_append", "fa_paged_attention", "fa_paged_weights", "fa_paged_evict"):
+        getattr(L, name).restype = I
     L.fa_check_device_status.argtypes = [P]
     L.fa_status_str.argtypes = [I]
     L.fa_status_str.restype = ctypes.c_char_p

@@ -135,6 +135,54 @@ struct DecodeAppendArgs {
 };
 cudaError_t launch_decode_append(const DecodeAppendArgs& a, int splits, void* ws, cudaStream_t s);
 
+// Paged caches (rope.cu, paged_attn.cu, paged_weights.cu, paged_evict.cu); the arguments have been checked.
+struct RopeAppendArgs {
+  const fa_rows* q;  // nullable, with q_out
+  const fa_rows* k;
+  const fa_rows* v;
+  const fa_paged_cache* cache;
+  const fa_paged_batch* batch;
+  const float* cos_sin;
+  int table_positions, rotary_dim;
+  const int* positions;  // nullable
+  int interleaved;
+  const float* amax_k;  // per-head modes
+  const float* amax_v;
+  const fa_rows* q_out;
+  int* status;
+};
+struct PagedAttnArgs {
+  const fa_rows* q;
+  const fa_paged_cache* cache;
+  const fa_paged_batch* batch;
+  int causal;
+  float softmax_scale;
+  void* out;
+  float* lse;  // attention: nullable output; weights: input
+  int* status;
+  float* acc;  // weights only, from here
+  long long acc_stride;
+  int accumulate;
+};
+struct PagedEvictArgs {
+  const fa_paged_cache* cache;
+  const fa_paged_batch* batch;
+  const float* scores;
+  long long score_stride;
+  int budget, sink, recent;
+  int* kept;
+  int* new_lens;
+  float* scores_out;
+  int* status;
+};
+cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, const double* inv_freq, double factor,
+                              cudaStream_t s);
+cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s);
+size_t paged_attention_ws(int D);
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, cudaStream_t s);
+cudaError_t launch_paged_weights(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t s);
+
 cudaError_t launch_fill_empty_rows(void* out, float* lse, long long rows, int D, cudaStream_t s);
 
 }  // namespace faq

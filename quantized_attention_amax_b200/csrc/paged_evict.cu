@@ -1,0 +1,303 @@
+// paged_evict.cu -- eviction from a paged cache: keep the first `sink`, the last `recent` and the
+// highest-scored of the other tokens of each (sequence, kv head), and move the kept rows to the front.
+//
+// One cluster of CTAs per (sequence, kv head), in one launch:
+//   1. the score that the last kept candidate has, by radix selection on the scores' bits (11, 11
+//      and 10 of them, highest first): each CTA counts its slice's digits in shared memory, the counts
+//      of the cluster's CTAs are added through distributed shared memory;
+//   2. the kept indices in order: each warp counts its part's scores above the threshold and equal to
+//      it, the counts before it give its places, and of the equal ones the lowest indices are taken;
+//   3. the rows, in rounds: every CTA of the cluster brings its share of the round's kept rows into
+//      shared memory, a cluster barrier, then all are written.  A row's new index is never above its
+//      old one, so what a round writes lies below every row that later rounds read: the barrier between a
+//      round's reads and its writes is all the order that moving in place needs.
+// The scores (once) and the kept rows (read and written once) bound it; slices are kept in shared
+// memory between the passes.  The cluster is as large as the GPU's SMs allow for the number of
+// (sequence, head) pairs, up to 8 CTAs.
+#include <cooperative_groups.h>
+
+#include "paged_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace faq {
+namespace {
+using namespace paged;
+
+constexpr int ET = 512;             // threads per CTA
+constexpr int EW = ET / 32;
+constexpr int BINS = 2048;
+constexpr int STAGE_BYTES = 144 * 1024;  // keys of the slice, then staged rows
+
+struct EvictP {
+  Cache c;
+  Batch bt;
+  const float* scores;
+  long long score_stride;
+  int budget, sink, recent;
+  int* kept;
+  int* new_lens;
+  float* scores_out;
+  int* status;
+};
+
+// Order-preserving bits: NaN lowest, then -inf .. +inf, the two zeros equal.
+__device__ __forceinline__ uint32_t score_bits(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct EvictSmem {
+  uint32_t hist[2][BINS];
+  uint32_t warp_sum[EW];
+  uint32_t warp_gt[EW], warp_eq[EW];
+  uint32_t cta_gt, cta_eq;
+  uint32_t digit, above;  // the digit holding the threshold, and how many lie above it
+};
+
+template <int D>
+__global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
+  extern __shared__ __align__(16) uint8_t stage[];
+  __shared__ EvictSmem sm;
+  cg::cluster_group cl = cg::this_cluster();
+  const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bh = blockIdx.x / cs;
+  const int b = bh / p.c.H, h = bh - b * p.c.H;
+  const int n = __ldg(p.bt.lens + b);
+  if (n < 0 || n > ((long long)p.bt.max_pages << p.c.page_shift) || n > p.score_stride) {  // uniform in the cluster
+    if (tid == 0) bad(p.status, 231);
+    return;
+  }
+  const float* sc = p.scores + (long long)bh * p.score_stride;
+  int* kept = p.kept + (long long)bh * p.budget;
+  float* so = p.scores_out ? p.scores_out + (long long)bh * p.score_stride : nullptr;
+  const int keep = min(n, p.budget);
+  const int gt0 = rank * ET + tid, gts = cs * ET;  // the thread among the cluster's
+  if (h == 0 && gt0 == 0) p.new_lens[b] = keep;
+  for (int i = keep + gt0; i < p.budget; i += gts) kept[i] = -1;
+  if (so)
+    for (long long i = keep + gt0; i < p.score_stride; i += gts) so[i] = 0.0f;
+  if (n <= p.budget) {
+    for (int i = gt0; i < n; i += gts) {
+      kept[i] = i;
+      if (so) so[i] = __ldg(sc + i);
+    }
+    return;
+  }
+
+  // ---- 1. the threshold: the need-th highest of the candidates [sink, n - recent)
+  const int cand = n - p.recent - p.sink;
+  int need = p.budget - p.sink - p.recent;  // 0 <= need < cand
+  const int chunk = (cand + cs - 1) / cs;
+  const int lo = min(cand, rank * chunk), cnt = min(cand, lo + chunk) - lo;
+  const float* mine = sc + p.sink + lo;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(stage);
+  constexpr int CAP = STAGE_BYTES / 4;
+  const int cached = min(cnt, CAP);
+  for (int i = tid; i < cached; i += ET) keys[i] = score_bits(__ldg(mine + i));
+  auto key = [&](int i) { return i < CAP ? keys[i] : score_bits(__ldg(mine + i)); };
+
+  uint32_t thr = 0;
+  if (need > 0) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t mask = pass == 2 ? 1023u : 2047u;
+      uint32_t* hist = sm.hist[pass & 1];
+      for (int i = tid; i < BINS; i += ET) hist[i] = 0;
+      __syncthreads();
+      const uint32_t hi_mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+      for (int i = tid; i < cnt; i += ET) {
+        const uint32_t k = key(i);
+        if ((k & hi_mask) == thr) atomicAdd(&hist[(k >> shift) & mask], 1u);
+      }
+      cl.sync();
+      // this thread's four bins, highest first, summed over the cluster
+      uint32_t mybin[4], sum = 0;
+      const int top = BINS - 1 - 4 * tid;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mybin[q] = 0;
+      for (int r = 0; r < cs; ++r) {
+        const uint32_t* rh = cl.map_shared_rank(hist, r);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mybin[q] += rh[top - q];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += mybin[q];
+      uint32_t incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      if (lane == 31) sm.warp_sum[warp] = incl;
+      __syncthreads();
+      uint32_t before = incl - sum;
+      for (int w = 0; w < warp; ++w) before += sm.warp_sum[w];
+      if (before < (uint32_t)need && before + sum >= (uint32_t)need) {  // one thread of the CTA
+        int q = 0;
+        while (before + mybin[q] < (uint32_t)need) before += mybin[q++];
+        sm.digit = (uint32_t)(top - q);
+        sm.above = before;
+      }
+      __syncthreads();
+      thr |= sm.digit << shift;
+      need -= (int)sm.above;
+      __syncthreads();  // digit, above and warp_sum are read
+    }
+  }
+  // need: how many of the scores equal to thr are kept (with need == 0 from the start: none at all)
+  const bool none = p.budget - p.sink - p.recent == 0;
+
+  // ---- 2. the kept indices, in order
+  const int per = ((cnt + EW - 1) / EW + 31) / 32 * 32;
+  const int w0 = min(cnt, warp * per), w1 = min(cnt, w0 + per);
+  uint32_t gt = 0, eq = 0;
+  __syncthreads();
+  if (!none)
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+      const uint32_t k = i < w1 ? key(i) : 0;
+      gt += __popc(__ballot_sync(0xffffffffu, i < w1 && k > thr));
+      eq += __popc(__ballot_sync(0xffffffffu, i < w1 && k == thr));
+    }
+  if (lane == 0) {
+    sm.warp_gt[warp] = gt;
+    sm.warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t a = 0, e = 0;
+    for (int w = 0; w < EW; ++w) {
+      a += sm.warp_gt[w];
+      e += sm.warp_eq[w];
+    }
+    sm.cta_gt = a;
+    sm.cta_eq = e;
+  }
+  cl.sync();
+  uint32_t gt_before = 0, eq_before = 0;
+  for (int r = 0; r < rank; ++r) {
+    gt_before += *cl.map_shared_rank(&sm.cta_gt, r);
+    eq_before += *cl.map_shared_rank(&sm.cta_eq, r);
+  }
+  for (int w = 0; w < warp; ++w) {
+    gt_before += sm.warp_gt[w];
+    eq_before += sm.warp_eq[w];
+  }
+  const unsigned below = (1u << lane) - 1u;
+  if (!none)
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+      const uint32_t k = i < w1 ? key(i) : 0;
+      const bool is_gt = i < w1 && k > thr, is_eq = i < w1 && k == thr;
+      const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+      const uint32_t e = eq_before + __popc(be & below);  // equal scores before this one
+      if (is_gt || (is_eq && e < (uint32_t)need)) {
+        const uint32_t place = gt_before + __popc(bg & below) + min(e, (uint32_t)need);
+        kept[p.sink + place] = p.sink + lo + i;
+      }
+      gt_before += __popc(bg);
+      eq_before += __popc(be);
+    }
+  for (int i = gt0; i < p.sink; i += gts) kept[i] = i;
+  for (int i = gt0; i < p.recent; i += gts) kept[p.budget - p.recent + i] = n - p.recent + i;
+  cl.sync();  // the list is written; the slices' keys are read
+
+  // ---- 3. the rows
+  constexpr int CH = D / 16;                         // 16-byte chunks per code row
+  constexpr int ROW = 2 * D + 8;                     // K, V codes; then the scales
+  constexpr int R = STAGE_BYTES / ROW / 32 * 32;     // rows per CTA and round
+  uint4* srow = reinterpret_cast<uint4*>(stage);     // [R][2 CH]
+  float2* sscale = reinterpret_cast<float2*>(stage + R * 2 * D);
+  for (int base = 0; base < keep; base += cs * R) {
+    const int d0 = base + rank * R, rows = max(0, min(keep - d0, R));
+    // 2 CH lanes a row: the K chunks, then the V chunks
+    const int c = tid % (2 * CH), r0 = tid / (2 * CH);
+    constexpr int RS = ET / (2 * CH);
+    const uint8_t* codes = c < CH ? p.c.k : p.c.v;
+    const int cc = c % CH;
+#pragma unroll 4
+    for (int r = r0; r < rows; r += RS) {
+      const int f = __ldcg(kept + d0 + r);
+      if (f == d0 + r) continue;
+      const int pg = page_of(p.bt, p.c, b, f, p.status, 232);
+      if (pg < 0) continue;
+      srow[r * 2 * CH + c] = __ldcg(reinterpret_cast<const uint4*>(codes + p.c.row(pg, h, f & p.c.page_mask)) + cc);
+    }
+    for (int r = tid; r < rows; r += ET) {
+      const int f = __ldcg(kept + d0 + r);
+      if (so) so[d0 + r] = __ldg(sc + f);
+      if (!p.c.per_token || f == d0 + r) continue;
+      const int pg = page_of(p.bt, p.c, b, f, p.status, 232);
+      if (pg < 0) continue;
+      const long long si = p.c.scale(pg, h, f & p.c.page_mask);
+      sscale[r] = make_float2(__ldcg(p.c.ks + si), __ldcg(p.c.vs + si));
+    }
+    cl.sync();  // every row of the round is read
+    uint8_t* dst = c < CH ? p.c.k : p.c.v;
+#pragma unroll 4
+    for (int r = r0; r < rows; r += RS) {
+      const int d = d0 + r, f = __ldcg(kept + d);
+      if (f == d) continue;
+      const int pg = page_of(p.bt, p.c, b, d, p.status, 232);
+      if (pg < 0 || page_of(p.bt, p.c, b, f, p.status, 232) < 0) continue;
+      reinterpret_cast<uint4*>(dst + p.c.row(pg, h, d & p.c.page_mask))[cc] = srow[r * 2 * CH + c];
+    }
+    if (p.c.per_token)
+      for (int r = tid; r < rows; r += ET) {
+        const int d = d0 + r, f = __ldcg(kept + d);
+        if (f == d) continue;
+        const int pg = page_of(p.bt, p.c, b, d, p.status, 232);
+        if (pg < 0 || page_of(p.bt, p.c, b, f, p.status, 232) < 0) continue;
+        const long long si = p.c.scale(pg, h, d & p.c.page_mask);
+        p.c.ks[si] = sscale[r].x;
+        p.c.vs[si] = sscale[r].y;
+      }
+    __syncthreads();  // the staging is free
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const EvictP& p, cudaStream_t s) {
+  auto kern = paged_evict_kernel<D>;
+  cudaError_t e;
+  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), STAGE_BYTES)) != cudaSuccess) return e;
+  const long long items = (long long)p.bt.B * p.c.H;
+  int cs = 8;
+  while (cs > 1 && items * cs > sm_count()) cs >>= 1;
+  if (items * cs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * cs));
+  cfg.blockDim = dim3(ET);
+  cfg.dynamicSmemBytes = STAGE_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cs;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t s) {
+  EvictP p = {};
+  p.c = paged_cache_of(*a.cache);
+  p.bt = paged_batch_of(*a.batch, 0);
+  p.scores = a.scores;
+  p.score_stride = a.score_stride;
+  p.budget = a.budget;
+  p.sink = a.sink;
+  p.recent = a.recent;
+  p.kept = a.kept;
+  p.new_lens = a.new_lens;
+  p.scores_out = a.scores_out;
+  p.status = a.status;
+  return a.cache->D == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
+}
+
+}  // namespace faq

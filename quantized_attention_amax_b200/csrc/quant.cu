@@ -32,23 +32,6 @@ __device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t a, uint32_t b) {
   return d;
 }
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-// Four fp32 values -> four E4M3 bytes (a in the lowest byte), RNE, saturating.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-
 // Eight fp32 values -> eight E2M1 nibbles (v[0] in the lowest nibble).
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   uint32_t r;
@@ -61,38 +44,6 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
       : "=r"(r)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
-}
-
-// Int8 codes of four quotients, rounded half to even, on the FMA / ALU pipes (a float-to-integer
-// conversion would run on the quarter-rate XU pipe): adding 1.5 * 2^23 rounds to an integer in
-// the low mantissa bits (exact for |x| < 2^22), whose low byte is the two's-complement code;
-// three byte permutes pack the four codes.  SAT (static scales, which data can exceed): NaN -> 0
-// as a conversion gives, then a clamp to [-128, 127] (before or after rounding gives the same
-// integer, the bounds being integers).  Without SAT (per-token scales) |x / s| <= 127 holds by
-// construction, so no clamp is needed.
-template <bool SAT>
-__device__ __forceinline__ uint32_t s8x4(float a, float b, float c, float d) {
-  if (SAT) {
-    a = fminf(fmaxf(a == a ? a : 0.0f, -128.0f), 127.0f);
-    b = fminf(fmaxf(b == b ? b : 0.0f, -128.0f), 127.0f);
-    c = fminf(fmaxf(c == c ? c : 0.0f, -128.0f), 127.0f);
-    d = fminf(fmaxf(d == d ? d : 0.0f, -128.0f), 127.0f);
-  }
-  constexpr float kMagic = 12582912.0f;
-  asm("{\n\t.reg .b64 x, y, m;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\t"
-      "add.rn.f32x2 x, x, m;\n\tadd.rn.f32x2 y, y, m;\n\tmov.b64 {%0, %1}, x;\n\tmov.b64 {%2, %3}, y;\n\t}"
-      : "+f"(a), "+f"(b), "+f"(c), "+f"(d)
-      : "f"(kMagic));
-  const uint32_t ab = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);  // low bytes of a, b
-  const uint32_t cd = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
-  return __byte_perm(ab, cd, 0x5410);
-}
-
-// max(|a|, |b|) per half as above, but a NaN in either input gives NaN
-__device__ __forceinline__ uint32_t bf16x2_absmax_nan(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
 }
 
 // n / d for n < 2^32 by one multiply-high (T. Granlund and P. L. Montgomery, "Division by

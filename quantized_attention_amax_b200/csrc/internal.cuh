@@ -179,6 +179,8 @@ cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, const
                               cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s);
 size_t paged_attention_ws(int D);
+size_t paged_decode_ws();
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, int rows, void* ws, cudaStream_t s);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_paged_weights(const PagedAttnArgs& a, cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t s);

@@ -19,7 +19,7 @@
 // and the eight are merged at the item's end.
 #include <cuda_bf16.h>
 
-#include "paged_common.cuh"
+#include "paged_sched.cuh"
 
 namespace faq {
 namespace {
@@ -30,90 +30,9 @@ constexpr int SK = 32;        // keys per warp piece
 constexpr int UK = AW * SK;   // keys per unit
 constexpr int NST = 3;        // ring stages per warp
 constexpr float kPShift = 14.0f;  // probabilities are held as p 2^14: fp16 keeps 11 bits of them down to 2^-28
+constexpr float kPInv = 1.0f / 16384.0f;
 
-struct AttnP {
-  const __nv_bfloat16* q;
-  long long q_stride;
-  Cache c;
-  Batch bt;
-  int Hq, G, causal;
-  float scale_log2;
-  __nv_bfloat16* out;
-  float* lse;
-  float* part_o;   // [2 grid][16][D]
-  float2* part_ml; // [2 grid][16]
-  int* status;
-};
-
-// The units of sequence b: row blocks of 16 (rows = new tokens x group), key units each.
-struct Item {
-  int b, hk, rb;      // of the current unit
-  Seq s;
-  int nrb, nt;        // row blocks, key units per (row block)
-  long long first;    // first unit of this (b, hk, rb)
-};
-
-__device__ __forceinline__ void seq_units(const AttnP& p, int b, Seq& s, int& nrb, int& nt) {
-  s = load_seq(p.bt, p.c.page_shift, b, p.status, 211);
-  nrb = (s.m * p.G + 15) >> 4;
-  nt = s.m > 0 ? max(1, (s.n + UK - 1) / UK) : 0;
-}
-
-// All units of the batch (every lane of the warp gets the sum).
-__device__ __forceinline__ long long total_units(const AttnP& p, int lane) {
-  long long w = 0;
-  for (int b = lane; b < p.bt.B; b += 32) {
-    Seq s;
-    int nrb, nt;
-    seq_units(p, b, s, nrb, nt);
-    w += (long long)nrb * nt;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
-  return w * p.c.H;
-}
-
-// The item that holds unit u < total.
-__device__ __forceinline__ Item find_item(const AttnP& p, long long u, int lane) {
-  long long base = 0;
-  Item it = {};
-  for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
-    const int b = b0 + lane;
-    Seq s = {0, 0, 0};
-    int nrb = 0, nt = 0;
-    if (b < p.bt.B) seq_units(p, b, s, nrb, nt);
-    const long long mine = (long long)nrb * nt * p.c.H;
-    long long end = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, end, off);
-      if (lane >= off) end += o;
-    }
-    const unsigned after = __ballot_sync(0xffffffffu, base + end > u);
-    if (after) {
-      const int src = __ffs(after) - 1;
-      it.b = b0 + src;
-      it.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-      it.s.m = __shfl_sync(0xffffffffu, s.m, src);
-      it.s.n = __shfl_sync(0xffffffffu, s.n, src);
-      it.nrb = __shfl_sync(0xffffffffu, nrb, src);
-      it.nt = __shfl_sync(0xffffffffu, nt, src);
-      const long long start = base + __shfl_sync(0xffffffffu, end - mine, src);
-      const long long k = (u - start) / it.nt;  // (hk, rb) of the unit
-      it.hk = (int)(k / it.nrb);
-      it.rb = (int)(k - (long long)it.hk * it.nrb);
-      it.first = start + k * it.nt;
-      return it;
-    }
-    base += __shfl_sync(0xffffffffu, end, 31);
-  }
-  it.b = p.bt.B;
-  return it;
-}
-
-// Run c of `runs` equal ones; a grid larger than the units leaves its last CTAs idle, so no run is empty.
-__device__ __forceinline__ long long run_start(long long total, int c, int runs) { return total * c / runs; }
-__device__ __forceinline__ int run_count(long long total, int grid) { return total < grid ? (int)total : grid; }
+using PL = Plan<UK, 16, 1, 0x7FFFFFFF>;
 
 template <int D>
 struct AS {
@@ -141,12 +60,12 @@ __global__ void __launch_bounds__(AW * 32, 1) paged_attn_kernel(const AttnP p) {
   uint8_t* ring = smem + warp * L::WARP;
   const uint32_t ring_u = smem_u32(ring);
 
-  const long long total = total_units(p, lane);
+  const long long total = total_units<PL>(p, lane);
   const int runs = run_count(total, gridDim.x);
   if ((int)blockIdx.x >= runs) return;
   const long long u0 = run_start(total, blockIdx.x, runs), u1 = run_start(total, blockIdx.x + 1, runs);
   long long u = u0;
-  Item it = find_item(p, u, lane);
+  Item it = find_item<PL>(p, u, lane);
 
   while (u < u1) {
     const Seq s = it.s;
@@ -165,7 +84,7 @@ __global__ void __launch_bounds__(AW * 32, 1) paged_attn_kernel(const AttnP p) {
       const int r = it.rb * 16 + g + 8 * x;
       const int i = r / p.G;
       const bool ok = r < rows;
-      lim[x] = !ok ? -1 : p.causal ? min(s.n - 1, s.n - s.m + i) : s.n - 1;
+      lim[x] = row_limit(p, s, r);
       const __nv_bfloat16* src = p.q + (long long)(s.q0 + i) * p.q_stride + (long long)(it.hk * p.G + r - i * p.G) * D;
       uint4 raw[KC][2];
       float m = 0.0f;
@@ -441,86 +360,32 @@ __global__ void __launch_bounds__(AW * 32, 1) paged_attn_kernel(const AttnP p) {
         a.z += x.z;
         a.w += x.w;
       }
+      l *= kPInv;
+      a.x *= kPInv;
+      a.y *= kPInv;
+      a.z *= kPInv;
+      a.w *= kPInv;
       if (whole) {
         const int rr = it.rb * 16 + r;
         if (rr < rows) {
           const int i = rr / p.G, hq = it.hk * p.G + rr - i * p.G;
-          const float f = l > 0.0f || l != l ? (TOK ? 1.0f : __ldg(p.c.vs + it.hk)) / l : 0.0f;
+          const float f = row_factor(p, it.hk, l, m, m);
           const long long row = (long long)(s.q0 + i) * p.Hq + hq;
           const __nv_bfloat162 v0 = __floats2bfloat162_rn(a.x * f, a.y * f), v1 = __floats2bfloat162_rn(a.z * f, a.w * f);
           *reinterpret_cast<uint2*>(p.out + row * D + c * 4) =
               make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
-          if (c == 0 && p.lse) p.lse[row] = (m - kPShift + log2f(l)) * 0.69314718055994530942f;
+          if (c == 0 && p.lse) p.lse[row] = row_lse(l, m);
         }
       } else {
         *reinterpret_cast<float4*>(p.part_o + ((long long)slot * 16 + r) * D + c * 4) = a;
-        if (c == 0) p.part_ml[slot * 16 + r] = make_float2(m, l);
+        if (c == 0) p.part_ml[(long long)slot * 16 + r] = make_float4(m, l, m, 0.0f);
       }
     }
     __syncthreads();  // the ring is free again
 
     u = seg_end;
     if (u >= u1) break;
-    // the next item: next row block, kv head, or sequence with units
-    if (++it.rb == it.nrb) {
-      it.rb = 0;
-      if (++it.hk == p.c.H) {
-        it.hk = 0;
-        do {
-          if (++it.b >= p.bt.B) return;  // cannot be while the lengths stay as they were counted
-          seq_units(p, it.b, it.s, it.nrb, it.nt);
-        } while (it.nt == 0);
-      }
-    }
-    it.first = u;
-  }
-}
-
-// The merge of the items that a run's border cuts: CTA c of this grid takes the item that starts in
-// run c and ends past it, whose pieces lie in run c's last slot and the first slots of the runs after.
-template <int D, bool TOK>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const AttnP p) {
-  const int lane = threadIdx.x & 31;
-  const int c = blockIdx.x;
-  const long long total = total_units(p, lane);
-  const int runs = run_count(total, gridDim.x);
-  if (c >= runs) return;
-  const long long u0 = run_start(total, c, runs), u1 = run_start(total, c + 1, runs);
-  if (u1 >= total) return;
-  const Item it = find_item(p, u1 - 1, lane);
-  const long long item_end = it.first + it.nt;
-  if (item_end <= u1 || it.first < u0) return;
-  int last = c + 1;
-  while (run_start(total, last + 1, runs) < item_end) ++last;
-  const int slot0 = 2 * c + (it.first == u0 ? 0 : 1);
-  const int rows = it.s.m * p.G;
-  for (int idx = threadIdx.x; idx < 16 * D / 4; idx += blockDim.x) {
-    const int r = idx / (D / 4), ch = idx % (D / 4);
-    const int rr = it.rb * 16 + r;
-    if (rr >= rows) continue;
-    float m = -INFINITY;
-    for (int k = c; k <= last; ++k) m = fmaxf(m, __ldg(&p.part_ml[(k == c ? slot0 : 2 * k) * 16 + r].x));
-    float l = 0.0f;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = c; k <= last; ++k) {
-      const int slot = k == c ? slot0 : 2 * k;
-      const float2 v = __ldg(&p.part_ml[slot * 16 + r]);
-      if (v.x == -INFINITY) continue;
-      const float w = attn::ex2(v.x - m);
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_o + ((long long)slot * 16 + r) * D) + ch);
-      l += w * v.y;
-      a.x += w * x.x;
-      a.y += w * x.y;
-      a.z += w * x.z;
-      a.w += w * x.w;
-    }
-    const int i = rr / p.G, hq = it.hk * p.G + rr - i * p.G;
-    const float f = l > 0.0f || l != l ? (TOK ? 1.0f : __ldg(p.c.vs + it.hk)) / l : 0.0f;
-    const long long row = (long long)(it.s.q0 + i) * p.Hq + hq;
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(a.x * f, a.y * f), v1 = __floats2bfloat162_rn(a.z * f, a.w * f);
-    *reinterpret_cast<uint2*>(p.out + row * D + ch * 4) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
-    if (ch == 0 && p.lse) p.lse[row] = (m - kPShift + log2f(l)) * 0.69314718055994530942f;
+    if (!next_item<PL>(p, it)) return;  // cannot be while the lengths stay as they were counted
   }
 }
 
@@ -531,7 +396,7 @@ cudaError_t launch_d(const AttnP& p, int grid, cudaStream_t s) {
   if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), AS<D>::TOTAL)) != cudaSuccess) return e;
   kern<<<grid, AW * 32, AS<D>::TOTAL, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  paged_combine_kernel<D, TOK><<<grid, 128, 0, s>>>(p);
+  combine_kernel<PL, D><<<grid, 128, 0, s>>>(p, grid);
   return cudaGetLastError();
 }
 
@@ -549,27 +414,18 @@ cudaError_t launch_mode(const AttnP& p, int mode, int grid, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attention_ws(int D) {
-  const size_t slots = 2 * (size_t)sm_count();
-  return slots * 16 * (size_t)D * 4 + slots * 16 * 8;
+  const size_t n = plan_ws<PL>(D, sm_count());
+  return D == 128 && paged_decode_ws() > n ? paged_decode_ws() : n;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
-  AttnP p = {};
   const int D = a.q->D;
-  p.q = static_cast<const __nv_bfloat16*>(a.q->data);
-  p.q_stride = a.q->stride;
-  p.c = paged_cache_of(*a.cache);
-  p.bt = paged_batch_of(*a.batch, a.q->T);
-  p.Hq = a.q->H;
-  p.G = a.q->H / a.cache->H;
-  p.causal = a.causal;
-  p.scale_log2 = (a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-  p.out = static_cast<__nv_bfloat16*>(a.out);
-  p.lse = a.lse;
-  p.status = a.status;
+  const int max_q = a.batch->cu_q ? (a.batch->max_q > 0 ? min(a.batch->max_q, a.q->T) : a.q->T) : 1;
+  const long long rows = (long long)max_q * (a.q->H / a.cache->H);
+  if (D == 128 && rows <= 16 && a.cache->pages > 0) return launch_paged_decode(a, (int)rows, ws, s);
+  AttnP p = paged_attn_params(a);
   const int grid = sm_count();
-  p.part_o = static_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * grid * 16 * D);
+  plan_carve<PL>(p, ws, D, grid);
   return D == 128 ? launch_mode<128>(p, a.cache->mode, grid, s) : launch_mode<64>(p, a.cache->mode, grid, s);
 }
 

@@ -1,0 +1,230 @@
+// paged_sched.cuh -- how the paged attention kernels share out a ragged batch.
+//
+// The work of one call is a row of units: sequence by sequence, kv head by kv head, row block by row
+// block (RB query rows: new tokens x the group's heads), UK keys to a unit.  The units are counted on the device
+// from the batch's lengths, and CTA c of `runs` takes the c-th of as many equal runs of consecutive units,
+// so a ragged batch balances whatever its lengths, and a captured graph follows lengths that change.  An
+// item -- one row block's units -- that a run covers wholly is written out by that CTA; the pieces of items that a
+// run's border cuts are left as partial results (O, m, l), at most two a run: the one at the run's
+// start in slot 0, any later one in slot 1.
+#pragma once
+
+#include "paged_common.cuh"
+
+namespace faq {
+namespace paged {
+
+struct AttnP {
+  const __nv_bfloat16* q;
+  long long q_stride;
+  Cache c;
+  Batch bt;
+  int Hq, G, causal;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;    // [2 runs][rows of a block][D]: sums of p s_v v in units of 2^mv
+  float4* part_ml;  // [2 runs][rows of a block]: m, l (sum of p in units of 2^m), mv
+  int* status;
+};
+
+// Sequences whose row count lies in [MINR, MAXR] are this kernel's.
+template <int UK_, int RB_, int MINR_, int MAXR_>
+struct Plan {
+  static constexpr int UK = UK_, RB = RB_, MINR = MINR_, MAXR = MAXR_;
+};
+
+struct Item {
+  int b, hk, rb;    // sequence, kv head, row block
+  Seq s;
+  int nrb, nt;      // the sequence's row blocks, units of each
+  long long first;  // first unit of the item
+};
+
+template <typename PL>
+__device__ __forceinline__ void seq_units(const AttnP& p, int b, Seq& s, int& nrb, int& nt) {
+  s = load_seq(p.bt, p.c.page_shift, b, p.status, 211);
+  const long long rows = (long long)s.m * p.G;
+  const bool mine = rows >= PL::MINR && rows <= PL::MAXR;
+  nrb = mine ? (int)((rows + PL::RB - 1) / PL::RB) : 0;
+  nt = mine ? max(1, (s.n + PL::UK - 1) / PL::UK) : 0;  // a sequence without keys still has rows to write
+}
+
+// All units of the batch (every lane of the warp gets the sum).
+template <typename PL>
+__device__ __forceinline__ long long total_units(const AttnP& p, int lane) {
+  long long w = 0;
+  for (int b = lane; b < p.bt.B; b += 32) {
+    Seq s;
+    int nrb, nt;
+    seq_units<PL>(p, b, s, nrb, nt);
+    w += (long long)nrb * nt;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+  return w * p.c.H;
+}
+
+// The item that holds unit u < total (a warp's work).
+template <typename PL>
+__device__ __forceinline__ Item find_item(const AttnP& p, long long u, int lane) {
+  long long base = 0;
+  Item it = {};
+  for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
+    const int b = b0 + lane;
+    Seq s = {0, 0, 0};
+    int nrb = 0, nt = 0;
+    if (b < p.bt.B) seq_units<PL>(p, b, s, nrb, nt);
+    const long long mine = (long long)nrb * nt * p.c.H;
+    long long end = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, end, off);
+      if (lane >= off) end += o;
+    }
+    const unsigned after = __ballot_sync(0xffffffffu, base + end > u);
+    if (after) {
+      const int src = __ffs(after) - 1;
+      it.b = b0 + src;
+      it.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+      it.s.m = __shfl_sync(0xffffffffu, s.m, src);
+      it.s.n = __shfl_sync(0xffffffffu, s.n, src);
+      it.nrb = __shfl_sync(0xffffffffu, nrb, src);
+      it.nt = __shfl_sync(0xffffffffu, nt, src);
+      const long long start = base + __shfl_sync(0xffffffffu, end - mine, src);
+      const long long k = (u - start) / it.nt;  // (hk, rb) of the unit
+      it.hk = (int)(k / it.nrb);
+      it.rb = (int)(k - (long long)it.hk * it.nrb);
+      it.first = start + k * it.nt;
+      return it;
+    }
+    base += __shfl_sync(0xffffffffu, end, 31);
+  }
+  it.b = p.bt.B;
+  return it;
+}
+
+// The item after `it`: next row block, kv head, or sequence with units.  False past the last.
+template <typename PL>
+__device__ __forceinline__ bool next_item(const AttnP& p, Item& it) {
+  it.first += it.nt;
+  if (++it.rb < it.nrb) return true;
+  it.rb = 0;
+  if (++it.hk < p.c.H) return true;
+  it.hk = 0;
+  do {
+    if (++it.b >= p.bt.B) return false;
+    seq_units<PL>(p, it.b, it.s, it.nrb, it.nt);
+  } while (it.nt == 0);
+  return true;
+}
+
+// Run c of `runs` equal ones; a grid larger than the units leaves its last CTAs idle, so no run is empty.
+__device__ __forceinline__ long long run_start(long long total, int c, int runs) { return total * c / runs; }
+__device__ __forceinline__ int run_count(long long total, int grid) { return total < grid ? (int)total : grid; }
+
+// The last key that row r of the item's sequence sees (-1: none; rows past the sequence's: -1).
+__device__ __forceinline__ int row_limit(const AttnP& p, const Seq& s, int r) {
+  const int i = r / p.G;
+  return i >= s.m ? -1 : p.causal ? min(s.n - 1, s.n - s.m + i) : s.n - 1;
+}
+
+// One row's result from its merged sums: bf16 values a f, and the LSE.
+__device__ __forceinline__ float row_factor(const AttnP& p, int hk, float l, float m, float mv) {
+  if (!(l > 0.0f) && l == l) return 0.0f;  // no key seen
+  return (p.c.per_token ? attn::ex2(mv - m) : __ldg(p.c.vs + hk)) / l;
+}
+__device__ __forceinline__ float row_lse(float l, float m) { return (m + log2f(l)) * 0.69314718055994530942f; }
+
+// The merge of the items that a run's border cuts: CTA c takes the item that starts in run c and
+// ends past it, whose pieces lie in run c's slot and in slot 0 of the runs after it.
+template <typename PL, int D>
+__global__ void __launch_bounds__(128) combine_kernel(const AttnP p, int grid) {
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  const long long total = total_units<PL>(p, lane);
+  const int runs = run_count(total, grid);
+  if (c >= runs) return;
+  const long long u0 = run_start(total, c, runs), u1 = run_start(total, c + 1, runs);
+  if (u1 >= total) return;
+  const Item it = find_item<PL>(p, u1 - 1, lane);
+  const long long item_end = it.first + it.nt;
+  if (item_end <= u1 || it.first < u0) return;
+  int last = c + 1;
+  while (run_start(total, last + 1, runs) < item_end) ++last;
+  const int slot0 = 2 * c + (it.first == u0 ? 0 : 1);
+  const int rows = min(it.s.m * p.G - it.rb * PL::RB, PL::RB);
+  // several CTAs (blockIdx.y) share a block's rows
+  for (int idx = blockIdx.y * blockDim.x + threadIdx.x; idx < rows * (D / 4); idx += gridDim.y * blockDim.x) {
+    const int r = idx / (D / 4), ch = idx % (D / 4);
+    float m = -INFINITY, mv = -INFINITY;
+    for (int k = c; k <= last; ++k) {
+      const float4 v = __ldg(p.part_ml + (long long)(k == c ? slot0 : 2 * k) * PL::RB + r);
+      m = fmaxf(m, v.x);
+      mv = fmaxf(mv, v.z);
+    }
+    float l = 0.0f;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = c; k <= last; ++k) {
+      const long long row = (long long)(k == c ? slot0 : 2 * k) * PL::RB + r;
+      const float4 v = __ldg(p.part_ml + row);
+      if (v.x > -INFINITY) l += attn::ex2(v.x - m) * v.y;
+      if (v.z > -INFINITY) {
+        const float w = attn::ex2(v.z - mv);
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_o + row * D) + ch);
+        a.x += w * x.x;
+        a.y += w * x.y;
+        a.z += w * x.z;
+        a.w += w * x.w;
+      }
+    }
+    const int rr = it.rb * PL::RB + r;
+    const int i = rr / p.G, hq = it.hk * p.G + rr - i * p.G;
+    const float f = row_factor(p, it.hk, l, m, mv);
+    const long long row = (long long)(it.s.q0 + i) * p.Hq + hq;
+    const __nv_bfloat162 v0 = __floats2bfloat162_rn(a.x * f, a.y * f), v1 = __floats2bfloat162_rn(a.z * f, a.w * f);
+    *reinterpret_cast<uint2*>(p.out + row * D + ch * 4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+    if (ch == 0 && p.lse) p.lse[row] = row_lse(l, m);
+  }
+}
+
+// Workspace of a kernel of that plan with `grid` CTAs.
+template <typename PL>
+inline size_t plan_ws(int D, int grid) {
+  return (size_t)2 * grid * PL::RB * ((size_t)D * 4 + 16);
+}
+template <typename PL>
+inline void plan_carve(AttnP& p, void* ws, int D, int grid) {
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float4*>(p.part_o + (size_t)2 * grid * PL::RB * D);
+}
+
+}  // namespace paged
+
+// A call's parameters but for the workspace.
+inline paged::AttnP paged_attn_params(const PagedAttnArgs& a) {
+  paged::AttnP p = {};
+  p.q = static_cast<const __nv_bfloat16*>(a.q->data);
+  p.q_stride = a.q->stride;
+  p.c = paged_cache_of(*a.cache);
+  p.bt = paged_batch_of(*a.batch, a.q->T);
+  p.Hq = a.q->H;
+  p.G = a.q->H / a.cache->H;
+  p.causal = a.causal;
+  p.scale_log2 = (a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf((float)a.q->D)) * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  return p;
+}
+
+// Tensor map over a cache's codes: boxes of one page's (at most `keys`) rows of one head, 128-byte
+// rows with the 128-byte swizzle (64-byte rows: the 64-byte one).  A page index past the pool reads zeros.
+inline cudaError_t make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache& c, int keys) {
+  const int rows = c.page_size < keys ? c.page_size : keys;
+  // the layouts' [pages, H, page, D] and [pages, page, H, D] are those of a [B, H, S, D] tensor
+  return attn::make_code_map(map, base, c.pages, c.H, c.page_size, c.D, c.layout, rows);
+}
+
+}  // namespace faq

@@ -85,6 +85,9 @@ def attend(q, cache, table, lens, qlens, causal, scale=None):
             see = visible(n, m, causal)
             for h in range(H):
                 k, v = head_rows(cache, "k", h, pg, o), head_rows(cache, "v", h, pg, o)
+                sv = cache["vs"].to(torch.float64)
+                sv = sv[h].expand(n) if cache["mode"] in PER_HEAD else sv[pg, h, o]
+                code = v.abs() / sv[:, None]
                 for r in range(h * G, h * G + G):
                     x, ax = scores(q[t:t + m, r], k, scale)
                     x = x.masked_fill(~see, -torch.inf)
@@ -96,10 +99,16 @@ def attend(q, cache, table, lens, qlens, causal, scale=None):
                     # scaled and shifted in the exponent: 4 roundings of 2^-24 of |x| + |max| each
                     xe = torch.where(see, ax * (D + 8) * 2.0 ** -24 + x.abs().nan_to_num(posinf=0.0) * 2.0 ** -21, 0.0)
                     big = xe.amax(-1) + 2.0 ** -20
-                    # p enters the product as fp16: half a step 2^-11; bf16 output: half a step 2^-8;
-                    # p 2^14 below fp16's normals: half a step 2^-25, of the row's largest p = p_max: 2^-39 p_max
-                    pe = p * (2.0 ** -11 + 2.0 * big[:, None]) + p.amax(-1, keepdim=True) * 2.0 ** -38
-                    tol[t:t + m, r] = out[t:t + m, r].abs() * 2.0 ** -8 + (1 + 2.0 ** -7) * (pe @ v.abs()) + 1e-30
+                    # a factor w_j = p_j s_v(j) enters the product with at least 11 bits (half a step 2^-11: fp16,
+                    # or three E4M3 digits of 4 bits), but no finer than a fixed step below the row's largest
+                    # w: fp16 of w 2^14 has steps 2^-24 / 2^14, three E4M3 digits of 256 w have a last step of
+                    # 2^-9 / 256 / 256 = 2^-25 (half: 2^-26), 24-bit integers 2^-24 (half: 2^-25, and 2^-24 where w = 1
+                    # is held as 1 - 2^-24): at most 2^-24 of the largest, times the key's code.
+                    # bf16 output: half a step 2^-8.
+                    pe = p * (2.0 ** -11 + 2.0 * big[:, None])
+                    top = (p * sv).amax(-1, keepdim=True) * 2.0 ** -24
+                    tol[t:t + m, r] = out[t:t + m, r].abs() * 2.0 ** -8 + (1 + 2.0 ** -7) * (
+                        pe @ v.abs() + top * (see.to(torch.float64) @ code)) + 1e-30
                     ltol[t:t + m, r] = 2 * big + z.abs().nan_to_num(posinf=0.0) * 2.0 ** -22
         t += m
     return out, lse, tol, ltol

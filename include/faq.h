@@ -354,7 +354,7 @@ FAQ_API size_t fa_attention_workspace_size_qkv(const fa_qtensor* q, const fa_qte
  * would have to be requantized by an append).
  * codes: one byte each, [pages, H, page_size, D] (BNSD) or
  * [pages, page_size, H, D] (BSND), 16-byte aligned.  D: 64 or 128.
- * page_size: a power of two from 16 to 1024. */
+ * pages: at least 1.  page_size: a power of two from 16 to 1024. */
 typedef struct {
   void* k_codes;
   void* v_codes;

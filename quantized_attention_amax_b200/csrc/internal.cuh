@@ -178,8 +178,10 @@ struct PagedEvictArgs {
 cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, const double* inv_freq, double factor,
                               cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s);
-size_t paged_attention_ws(int D);
+size_t paged_attention_ws(const PagedAttnArgs& a);
 size_t paged_decode_ws();
+size_t paged_chunk_ws(int D);
+cudaError_t launch_paged_chunk(const PagedAttnArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int rows, void* ws, cudaStream_t s);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_paged_weights(const PagedAttnArgs& a, cudaStream_t s);

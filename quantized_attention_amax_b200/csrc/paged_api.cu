@@ -20,13 +20,13 @@ fa_status check_cache(const fa_paged_cache* c) {
   if (!c) return FA_ERR_INVALID_ARG;
   if (!per_head(c->mode) && c->mode != FA_MODE_INT8_PER_TOKEN && c->mode != FA_MODE_FP8_PER_TOKEN)
     return FA_ERR_UNSUPPORTED;
-  if (c->pages < 0 || c->H < 1 || (c->layout != FA_LAYOUT_BNSD && c->layout != FA_LAYOUT_BSND)) return FA_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->H < 1 || (c->layout != FA_LAYOUT_BNSD && c->layout != FA_LAYOUT_BSND)) return FA_ERR_INVALID_ARG;
   if (c->D != 64 && c->D != 128) return FA_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return FA_ERR_UNSUPPORTED;
   // strides inside a page are kept in 32 bits
   if ((long long)c->H * c->page_size * c->D > 0x7FFFFFFFLL) return FA_ERR_UNSUPPORTED;
   if (!c->k_scales || !c->v_scales || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4)) return FA_ERR_INVALID_ARG;
-  if (c->pages > 0 && (!c->k_codes || !c->v_codes || !aligned(c->k_codes, 16) || !aligned(c->v_codes, 16)))
+  if (!c->k_codes || !c->v_codes || !aligned(c->k_codes, 16) || !aligned(c->v_codes, 16))
     return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
@@ -112,7 +112,8 @@ fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, c
 
 size_t fa_paged_attention_workspace_size(const fa_rows* q, const fa_paged_cache* cache, const fa_paged_batch* batch) {
   if (check_attend(q, cache, batch) != FA_OK) return 0;
-  return paged_attention_ws(cache->D);
+  const PagedAttnArgs a = {q, cache, batch, 0, 0.0f, nullptr, nullptr, nullptr, nullptr, 0, 0};
+  return paged_attention_ws(a);
 }
 
 fa_status fa_paged_attention(const fa_rows* q, const fa_paged_cache* cache, const fa_paged_batch* batch, int causal,
@@ -122,10 +123,10 @@ fa_status fa_paged_attention(const fa_rows* q, const fa_paged_cache* cache, cons
   if (st != FA_OK) return st;
   if (q->T == 0 || batch->B == 0) return FA_OK;
   if (!out || !aligned(out, 16) || !aligned(lse, 4)) return FA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < paged_attention_ws(cache->D) || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
-  int* status = device_status_ptr();
-  if (!status) return FA_ERR_CUDA;
-  const PagedAttnArgs a = {q, cache, batch, causal ? 1 : 0, softmax_scale, out, lse, status, nullptr, 0, 0};
+  PagedAttnArgs a = {q, cache, batch, causal ? 1 : 0, softmax_scale, out, lse, nullptr, nullptr, 0, 0};
+  if (!workspace || ws_bytes < paged_attention_ws(a) || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
+  a.status = device_status_ptr();
+  if (!a.status) return FA_ERR_CUDA;
   return from_cuda(launch_paged_attention(a, workspace, reinterpret_cast<cudaStream_t>(s)));
 }
 

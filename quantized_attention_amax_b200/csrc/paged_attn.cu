@@ -413,20 +413,27 @@ cudaError_t launch_mode(const AttnP& p, int mode, int grid, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_attention_ws(int D) {
-  const size_t n = plan_ws<PL>(D, sm_count());
-  return D == 128 && paged_decode_ws() > n ? paged_decode_ws() : n;
+// Query rows per kv head that a sequence of the batch can have.
+static long long most_rows(const PagedAttnArgs& a) {
+  const int max_q = a.batch->cu_q ? (a.batch->max_q > 0 ? min(a.batch->max_q, a.q->T) : a.q->T) : 1;
+  return (long long)max_q * (a.q->H / a.cache->H);
+}
+
+size_t paged_attention_ws(const PagedAttnArgs& a) {
+  const int D = a.q->D;
+  if (D == 128 && most_rows(a) <= 16) return paged_decode_ws();
+  return paged_chunk_ws(D);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   const int D = a.q->D;
-  const int max_q = a.batch->cu_q ? (a.batch->max_q > 0 ? min(a.batch->max_q, a.q->T) : a.q->T) : 1;
-  const long long rows = (long long)max_q * (a.q->H / a.cache->H);
-  if (D == 128 && rows <= 16 && a.cache->pages > 0) return launch_paged_decode(a, (int)rows, ws, s);
-  AttnP p = paged_attn_params(a);
-  const int grid = sm_count();
-  plan_carve<PL>(p, ws, D, grid);
-  return D == 128 ? launch_mode<128>(p, a.cache->mode, grid, s) : launch_mode<64>(p, a.cache->mode, grid, s);
+  const long long rows = most_rows(a);
+  if (D == 128) {
+    // sequences of up to 16 query rows per kv head, then those of more
+    const cudaError_t e = launch_paged_decode(a, rows < 16 ? (int)rows : 16, ws, s);
+    if (e != cudaSuccess || rows <= 16) return e;
+  }
+  return launch_paged_chunk(a, ws, s);
 }
 
 }  // namespace faq

@@ -1,0 +1,793 @@
+// paged_chunk.cu -- attention of many query rows per kv head (chunks of prompts, drafts) over a paged
+// 8-bit cache, on the tensor cores' 16-bit kind.
+//
+// Long chunks are bound by the two products, 4 D flops per (row, key).  One CTA owns a block of 256 query rows
+// of one kv head (new tokens x the group's heads, so that every row of the block reads the same keys) as two
+// 128-row tiles, A and B, with one S and one O accumulator each in TMEM.  The MMA thread alternates the tiles
+//   QK_A(0) QK_B(0) | PV_A(0) QK_A(1) PV_B(0) QK_B(1) | PV_A(1) ...
+// so that the tensor pipe works on one tile while the other's softmax runs.  Blocks of at most 128 rows have
+// both tiles hold the same rows, A for the even and B for the odd key tiles: the two chains overlap as before,
+// and the merge of the two is done on the accumulators at the end.
+//
+// Codes are exact in fp16, and so are Q's rows scaled by powers of two (but for values 2^-29 below the row's
+// largest).  TMA brings the codes page by page to a staging ring, four warps convert them and write the swizzled
+// MMA operands (about 2000 warp instructions a tile, which fit beside the softmax of 256 rows: the cache needs
+// no conversion pass of its own).  P (fp16, up to 2^15) overwrites S in TMEM and is the A operand of
+// P V.  Scales: per head at the ends.  Per token: s_k on the scores, and s_v in the exponent, so that a row's
+// factors p s_v are held against the largest of them, whatever the scales' range:
+//   w_j = 2^(x_j + log2 s_v(j) - mv), mv the running maximum of x + log2 s_v;  sum p = 2^mv sum w_j / s_v(j).
+// Work is shared out as paged_sched.cuh says: a causal block counts the key tiles it sees.
+#include "paged_sched.cuh"
+
+namespace faq {
+namespace {
+using namespace paged;
+
+constexpr int BM = 128;       // rows per tile
+constexpr int TN = 128;       // keys per tile
+constexpr int NSG = 2;        // K and V stages
+constexpr int NSC = 3;        // scale stages (per-token modes)
+constexpr int CT = 512;       // warpgroups: pieces + loads, MMAs; converters; softmax A; softmax B
+constexpr int UR = 32;        // keys of a load unit
+constexpr int NU = 6;         // units in the staging ring
+constexpr int R0 = 56, RC = 72, RS = 192;  // the warpgroups' registers
+static_assert(128 * (R0 + RC + 2 * RS) <= CT * 128, "register split exceeds the launch");
+static_assert(R0 <= 128 && RC <= 128 && RS >= 128, "launched with 128 registers a thread: the first two warpgroups give some back");
+constexpr float kShift = 7.0f;  // P is held as p 2^7: fp16 keeps 11 bits of it down to 2^-21, and the running maximum may lag by 2^8
+// V scales below this are brought up to it, and their codes (exact otherwise) scaled down: 1 / s_v stays finite
+constexpr float kMinScale = 0x1p-90f;
+
+template <bool ALL>
+using CPL = Plan<TN, 2 * BM, ALL ? 1 : 17, 0x7FFFFFFF, true>;
+
+template <int D>
+struct CL {
+  static constexpr int NA = D / 64;                    // 128-byte atoms per fp16 row
+  static constexpr uint32_t ATOM = 128 * 128;          // bytes of one atom of 128 rows
+  static constexpr uint32_t TILE = NA * ATOM;
+  static constexpr uint32_t Q = 0;                     // two tiles
+  static constexpr uint32_t K = Q + 2 * TILE;          // NSG stages
+  static constexpr uint32_t V = K + NSG * TILE;        // NSG stages
+  static constexpr uint32_t SC = V + NSG * TILE;       // NSC x ([128] s_k, [128] log2 s_v, [128] 1 / s_v, [128] factors of V)
+  static constexpr uint32_t SCB = 4 * TN * 4;
+  static constexpr uint32_t ML = SC + NSC * SCB;       // [128] (m, l) of tile B (blocks of at most 128 rows)
+  static constexpr uint32_t PC = ML + BM * 8;          // NPC pieces
+  static constexpr uint32_t BAR = PC + 4 * 64;
+  static constexpr uint32_t UNIT = UR * D;             // raw codes
+  static constexpr uint32_t RAW = (BAR + 384 + 127) & ~127u;  // NU units on their way
+  static constexpr uint32_t TOTAL = RAW + NU * UNIT;
+  static constexpr uint32_t ALLOC = TOTAL + 1024;
+  static_assert(ALLOC <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t TS0 = 0, TO0 = 256, TO1 = 256 + D;  // TMEM columns: S_A, S_B at 0, 128
+};
+
+enum {
+  C_Q = 0,             // Q tiles written, and O free
+  C_KF = 1,            // [NSG]
+  C_KE = C_KF + NSG,
+  C_VF = C_KE + NSG,
+  C_VE = C_VF + NSG,
+  C_SF = C_VE + NSG,   // [2] S_A / S_B done
+  C_PF = C_SF + 2,     // [2] P stored
+  C_PV = C_PF + 2,     // [2] P V done
+  C_SCF = C_PV + 2,    // [NSC]
+  C_SCE = C_SCF + NSC, // [NSC]
+  C_ML = C_SCE + NSC,  // tile B's (m, l) written
+  C_FIN = C_ML + 1,
+  C_PCF = C_FIN + 1,   // [NPC] piece written
+  C_PCE = C_PCF + 4,   // [NPC] piece done with
+  C_RF = C_PCE + 4,    // [NU] staged unit landed
+  C_RE = C_RF + NU,    // [NU] staging slot free
+  C_COUNT = C_RE + NU
+};
+static_assert(C_COUNT * 8 + 8 <= 384, "barriers fit their region");
+
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// Four floats from shared memory, read here and now: the compiler would otherwise keep a tile's scales in
+// registers from one use to the next, and spill the scores for them.
+__device__ __forceinline__ float4 lds4(const float* p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(p)) : "memory");
+  return v;
+}
+
+// One piece of the CTA's run: key tiles [t0, t1) of a row block.  Warp 0 walks the run and leaves the
+// pieces in a ring in shared memory, so that the other warps spend no registers on the walk.
+struct Piece {
+  int b, hk, q0, m, n;  // the sequence and kv head
+  int row0;             // the block's first row
+  int t0, t1;
+  int kt[2];            // key tiles that the rows of tile A / B see
+  int dual;             // both tiles hold the block's rows (at most 128), and share the key tiles out
+  int whole;            // the piece is the whole item
+  int slot;             // of its partial result
+  int last;             // no piece follows
+  int pad[2];
+};
+constexpr int NPC = 4;  // pieces in the ring
+
+// Does tile x (A or B) have key tile t, and how many tiles has it?
+__device__ __forceinline__ bool has_tile(int t0, int t1, int kt, int dual, int x, int t) {
+  return t >= t0 && t < t1 && t < kt && (!dual || ((t - t0) & 1) == x);
+}
+__device__ __forceinline__ int tile_count(int t0, int t1, int kt, int dual, int x) {
+  const int n = min(t1, kt) - t0;
+  return n <= 0 ? 0 : dual ? (n + 1 - x) / 2 : n;
+}
+
+template <typename PL>
+__device__ __forceinline__ Piece make_piece(const AttnP& p, const Item& it, long long u, long long u0, long long u1) {
+  Piece o = {};
+  const Seq& s = it.s;
+  o.b = it.b;
+  o.hk = it.hk;
+  o.q0 = s.q0;
+  o.m = s.m;
+  o.n = s.n;
+  o.row0 = it.rb * PL::RB;
+  const int rows = min(s.m * p.G - o.row0, PL::RB);
+  o.dual = rows <= BM;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int end_row = o.row0 + (o.dual || x ? rows : BM) - 1;
+    const int end = p.causal ? min(s.n, s.n - s.m + end_row / p.G + 1) : s.n;
+    o.kt[x] = end > 0 ? (end + TN - 1) / TN : 0;
+  }
+  const long long item_end = it.first + it.nt, e = item_end < u1 ? item_end : u1;
+  o.t0 = (int)(u - it.first);
+  o.t1 = max(o.t0, min((int)(e - it.first), max(o.kt[0], o.kt[1])));
+  o.whole = u == it.first && item_end <= u1;
+  o.slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
+  o.last = item_end >= u1;
+  return o;
+}
+
+template <int D, bool FP8, bool TOK, bool ALL>
+__global__ void __launch_bounds__(CT, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnP p) {
+  using L = CL<D>;
+  using PL = CPL<ALL>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const long long total = total_units<PL>(p, lane);
+  const int runs = run_count(total, gridDim.x);
+  if ((int)blockIdx.x >= runs) return;
+  if (tid == 0) {
+    mbar_init(&bar[C_Q], 256);
+    for (int i = 0; i < NSG; ++i) {
+      mbar_init(&bar[C_KF + i], 4);
+      mbar_init(&bar[C_KE + i], 1);
+      mbar_init(&bar[C_VF + i], 4);
+      mbar_init(&bar[C_VE + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar[C_SF + i], 1);
+      mbar_init(&bar[C_PF + i], 4);
+      mbar_init(&bar[C_PV + i], 1);
+    }
+    for (int i = 0; i < NSC; ++i) {
+      mbar_init(&bar[C_SCF + i], 4);
+      mbar_init(&bar[C_SCE + i], 8);
+    }
+    mbar_init(&bar[C_ML], 128);
+    mbar_init(&bar[C_FIN], 1);
+    for (int i = 0; i < NPC; ++i) {
+      mbar_init(&bar[C_PCF + i], 1);
+      mbar_init(&bar[C_PCE + i], 13);  // the MMA thread, four converter warps, eight softmax warps
+    }
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(&bar[C_RF + i], 1);
+      mbar_init(&bar[C_RE + i], 4);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  auto wait = [&](int which, int phase, int where) { return mbar_wait(&bar[which], phase & 1, abort_flag, p.status, where); };
+  auto wwait = [&](int which, int phase, int where) { return __all_sync(0xffffffffu, wait(which, phase, where)); };
+  Piece* pieces = reinterpret_cast<Piece*>(smem + L::PC);
+
+  if (warp < 4) {
+    regs_dec<R0>();
+    if (warp == 0) {
+      // ------------------------------------------ the run's pieces, and their loads
+      const long long u0 = run_start(total, blockIdx.x, runs), u1 = run_start(total, blockIdx.x + 1, runs);
+      Item it = find_item<PL>(p, u0, lane);
+      const int box = min(UR, p.c.page_mask + 1), nbox = UR / box;  // a unit is one box, or two of 16-key pages
+      const bool bnsd = p.c.bnsd;
+      if (lane == 0) {
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+      }
+      long long u = u0;
+      int g = 0;  // units issued
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (k >= NPC && !(ok = wwait(C_PCE + k % NPC, k / NPC - 1, 240))) break;
+        Piece pc = make_piece<PL>(p, it, u, u0, u1);
+        u = it.first + it.nt;
+        if (!pc.last && !next_item<PL>(p, it)) pc.last = 1;  // cannot be while the lengths stay as they were counted
+        if (lane == 0) {
+          pieces[k % NPC] = pc;
+          mbar_arrive(&bar[C_PCF + k % NPC]);
+        }
+        // lane l < 8: the page of a tile's l-th 16 keys; past the end, or not a page: one past the pool, read as zeros
+        auto page = [&](int t) {
+          const int key = t * TN + (lane & 7) * 16;
+          int pg = p.c.pages;
+          if (t < pc.t1 && key < pc.n) {
+            pg = page_of(p.bt, p.c, pc.b, key, p.status, 212);
+            if (pg < 0) pg = p.c.pages;
+          }
+          return pg;
+        };
+        int pages = pc.t0 < pc.t1 ? page(pc.t0) : 0;
+        for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+          const int next = page(t + 1);  // its latency passes while this tile's units wait
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q, ++g) {
+            const int sl = g % NU, row = (q & 3) * UR + lane * box;  // this lane's box
+            const int pg = __shfl_sync(0xffffffffu, pages, (row >> 4) & 7);
+            if (g >= NU && !(ok = wwait(C_RE + sl, g / NU - 1, 238))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar[C_RF + sl], L::UNIT);
+            __syncwarp();
+            if (lane < nbox) {
+              const int off = (t * TN + row) & p.c.page_mask;
+              tma_load_4d(smem + L::RAW + sl * L::UNIT + lane * box * D, q < 4 ? &tmk : &tmv, &bar[C_RF + sl], 0,
+                          bnsd ? off : pc.hk, bnsd ? pc.hk : off, pg);
+            }
+          }
+          pages = next;
+        }
+        if (pc.last) break;
+      }
+      if (*abort_flag)  // let the issued loads land before the CTA can leave
+        for (int t = max(0, g - NU); t < g; ++t) mbar_drain(&bar[C_RF + t % NU], (t / NU) & 1);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ----------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        constexpr uint32_t id_qk = make_idesc(kAccF32, kFmtF16, kFmtF16, 0, 0, TN, BM);
+        constexpr uint32_t id_pv = make_idesc(kAccF32, kFmtF16, kFmtF16, 0, 1, D, BM);
+        const uint64_t dq = make_sdesc(smem_u32(smem + L::Q), 16, 1024, kSwz128);
+        const uint64_t dk = make_sdesc(smem_u32(smem + L::K), 16, 1024, kSwz128);
+        const uint64_t dv = make_sdesc(smem_u32(smem + L::V), L::ATOM, 1024, kSwz128);
+        const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+        int base = 0;           // tiles of the pieces before this one
+        int done[2] = {0, 0};   // tiles of A / B so far
+        bool ok = true, more = true;
+        for (int k = 0; ok && more; ++k) {
+          if (!(ok = wait(C_PCF + k % NPC, k / NPC, 239))) break;
+          const Piece& pc = pieces[k % NPC];
+          const int t0 = pc.t0, t1 = pc.t1, kt0 = pc.kt[0], kt1 = pc.kt[1], dual = pc.dual;
+          more = !pc.last;
+          mbar_arrive(&bar[C_PCE + k % NPC]);
+          if (!(ok = wait(C_Q, k, 241))) break;
+          tc_fence_after();
+          const int step = dual ? 2 : 1;
+          auto has = [&](int x, int t) { return has_tile(t0, t1, x ? kt1 : kt0, dual, x, t); };
+          auto qk = [&](int x, int t) {
+            const int j = base + t - t0;
+            if (!wait(C_KF + j % NSG, j / NSG, 242)) return false;
+            tc_fence_after();
+            const uint32_t ql = (uint32_t)dq + x * (L::TILE >> 4), kl = (uint32_t)dk + (j % NSG) * (L::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * L::ATOM + (kk % 4) * 32) >> 4;
+              mma_f16_lh(tbase + L::TS0 + x * 128, ql + off, k_hi, kl + off, k_hi, id_qk, kk > 0);
+            }
+            mma_commit(&bar[C_SF + x]);
+            if (x == 1 || !has(1, t)) mma_commit(&bar[C_KE + j % NSG]);  // the tile's last reader
+            return true;
+          };
+          auto pv = [&](int x, int t) {
+            const int j = base + t - t0;
+            if (!mbar_wait_spin(&bar[C_PF + x], done[x] & 1, abort_flag, p.status, 243)) return false;
+            if (!wait(C_VF + j % NSG, j / NSG, 244)) return false;
+            tc_fence_after();
+            const uint32_t vl = (uint32_t)dv + (j % NSG) * (L::TILE >> 4);
+#pragma unroll
+            for (int ks = 0; ks < TN / 16; ++ks)
+              mma_f16_ts_lh(tbase + (x ? L::TO1 : L::TO0), tbase + L::TS0 + x * 128 + ks * 8, vl + ((ks * 16 * 128) >> 4), v_hi,
+                            id_pv, (t >= t0 + step || ks > 0) ? 1u : 0u);
+            mma_commit(&bar[C_PV + x]);
+            if (x == 1 || !has(1, t)) mma_commit(&bar[C_VE + j % NSG]);
+            ++done[x];
+            return true;
+          };
+          // step r: P V of the tiles' r-th key tiles, each followed by its next Q K^T; r = -1: the first Q K^T
+#pragma unroll 1
+          for (int r = -step; ok && t0 + r < t1; r += step) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int t = t0 + r + (dual ? x : 0);
+              if (ok && r >= 0 && has(x, t)) ok = pv(x, t);
+              if (ok && has(x, t + step)) ok = qk(x, t + step);
+            }
+          }
+          base += t1 - t0;
+        }
+        mma_commit(&bar[C_FIN]);
+        mbar_drain(&bar[C_FIN], 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    regs_dec<RC>();
+    // ------------------------------------------- codes -> fp16 operand tiles
+    // A tile comes in eight units of 32 keys (four of K, four of V).  Thread: chunk c (16 codes, 32 bytes of fp16; D / 16
+    // lanes a row) of every RPP-th row.  Its key's scales come a tile ahead.
+    constexpr int LPR = D / 16, RPP = 128 / LPR, NP = UR / RPP;  // lanes per row, rows per pass, passes per unit
+    const int ct = tid - 128, c = ct % LPR, r0 = ct / LPR;
+    // the two 16-byte chunks of a row: lanes of the row's halves (D = 64: of odd rows) write them in turn, so that
+    // eight lanes cover the eight chunk positions of the banks
+    const int odd = (D == 128 ? c >> 2 : r0) & 1;
+    const uint32_t at0 = (c >> 2) * L::ATOM + swz128_offset(r0, 2 * (c & 3) + odd);
+    const uint32_t at1 = (c >> 2) * L::ATOM + swz128_offset(r0, 2 * (c & 3) + 1 - odd);
+    static_assert(RPP % 8 == 0, "passes keep the swizzle phase of the thread's first row");
+    int base = 0, g = 0;
+    bool ok = true, more = true;
+    for (int k = 0; ok && more; ++k) {
+      if (!(ok = wwait(C_PCF + k % NPC, k / NPC, 239))) break;
+      const Piece& pc = pieces[k % NPC];
+      const int hk = pc.hk, b = pc.b, n = pc.n, t0 = pc.t0, t1 = pc.t1;
+      const int lim_lo = p.causal ? n - pc.m : n - 1;
+      more = !pc.last;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C_PCE + k % NPC]);
+      float sk = 0.0f, sv = 0.0f;  // this thread's key of the coming tile
+      int raw_page = -1;           // its page in the tile after that, as it lies in the table
+      auto load_page = [&](int t) {
+        const int key = t * TN + ct;
+        return t < t1 && key < n ? __ldg(p.bt.table + (long long)b * p.bt.max_pages + (key >> p.c.page_shift)) : -1;
+      };
+      auto load_scales = [&](int t, int pg) {
+        sk = sv = 0.0f;
+        if ((unsigned)pg < (unsigned)p.c.pages) {
+          const long long si = p.c.scale(pg, hk, (t * TN + ct) & p.c.page_mask);
+          sk = __ldg(p.c.ks + si);
+          sv = __ldg(p.c.vs + si);
+        }
+      };
+      if (TOK && t0 < t1) {
+        load_scales(t0, load_page(t0));
+        raw_page = load_page(t0 + 1);
+      }
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int j = base + t - t0, st = j % NSG, ss = j % NSC;
+        float* sc = reinterpret_cast<float*>(smem + L::SC + ss * L::SCB);
+        if (TOK) {
+          // s_k, log2 s_v, 1 / s_v and the factor of the V codes (1 but for tiny scales).  A NaN or infinite
+          // s_v is given to the rows that see the key by s_k.
+          float f = 1.0f;
+          if (!(fabsf(sv) < INFINITY)) {
+            sk = __uint_as_float(0x7FC00000u);
+            f = 0.0f;
+            sv = kMinScale;
+          } else if (sv < kMinScale) {
+            f = sv * (1.0f / kMinScale);
+            sv = kMinScale;
+          }
+          if (j >= NSC && !(ok = wwait(C_SCE + ss, j / NSC - 1, 245))) break;
+          sc[ct] = sk;
+          sc[TN + ct] = log2f(sv);
+          sc[2 * TN + ct] = 1.0f / sv;
+          sc[3 * TN + ct] = f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C_SCF + ss]);
+          load_scales(t + 1, raw_page);
+          raw_page = load_page(t + 2);
+        }
+        // In a tile that not every row sees whole, V rows past the end are cleared, and rows with E4M3 NaN
+        // codes too (0 times NaN is NaN), whose key's K row becomes NaN for the rows that see it.
+        const bool edge = FP8 && t * TN + TN - 1 > lim_lo;
+        uint32_t clear = 0;  // bit NP u + q: pass q of unit u's rows
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u, ++g) {
+          const int sl = g % NU;
+          if (!(ok = wwait(C_RF + sl, g / NU, 237))) break;
+          if (u == 0 && j >= NSG && !(ok = wwait(C_KE + st, j / NSG - 1, 246))) break;
+          if (u == 4 && j >= NSG && !(ok = wwait(C_VE + st, j / NSG - 1, 247))) break;
+          if (u == 4 && TOK && !(ok = wwait(C_SCF + ss, j / NSC, 255))) break;  // the other warps' factors
+          uint32_t k_nan = 0;
+          if (edge && u < 4) {
+            static_assert(NU > 4, "unit u + 4 is in the ring while unit u is converted");
+            if (!(ok = wwait(C_RF + (g + 4) % NU, (g + 4) / NU, 236))) break;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(smem + L::RAW + ((g + 4) % NU) * L::UNIT + q * 2048 + ct * 16);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              bool nan = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) nan = nan || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+              const unsigned hit = __ballot_sync(0xffffffffu, nan);
+              const bool row_nan = (hit & (((1u << LPR) - 1u) << (lane / LPR * LPR))) != 0;
+              const bool past = t * TN + u * UR + r0 + q * RPP >= n;
+              if (row_nan || past) clear |= 1u << (NP * u + q);
+              if (row_nan && !past) k_nan |= 1u << q;
+            }
+          }
+          uint8_t* tile = smem + (u < 4 ? L::K : L::V) + st * L::TILE + (u & 3) * UR * 128;
+          const uint8_t* raw = smem + L::RAW + sl * L::UNIT + ct * 16;
+#pragma unroll
+          for (int q = 0; q < NP; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4*>(raw + q * 2048);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) codes4_to_h2<FP8>(w[e], h[2 * e], h[2 * e + 1]);
+            if (FP8 && edge) {
+              const bool zero = u >= 4 && ((clear >> (NP * (u - 4) + q)) & 1u), nan = (k_nan >> q) & 1u;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) h[e] = zero ? 0u : nan ? 0x7FFF7FFFu : h[e];
+            }
+            if (TOK && u >= 4) {
+              const float f = sc[3 * TN + (u - 4) * UR + r0 + q * RPP];
+              if (f != 1.0f) {
+                const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), f2);
+                  h[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+              }
+            }
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(tile + at0 + q * RPP * 128) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(tile + at1 + q * RPP * 128) = odd ? lo : hi;
+          }
+          if ((u & 3) == 3) fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar[C_RE + sl]);
+            if ((u & 3) == 3) mbar_arrive(&bar[(u < 4 ? C_KF : C_VF) + st]);
+          }
+        }
+      }
+      base += t1 - t0;
+    }
+  } else {
+    regs_inc<RS>();
+    // ---------------------------------------------------------------- softmax
+    const int x = (warp - 8) >> 2;
+    const int i = tid - 256 - x * 128;  // row of the tile, TMEM lane
+    const uint32_t loff = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + L::TS0 + x * 128;
+    const uint32_t tO = tbase + (x ? L::TO1 : L::TO0);
+    float2* ml = reinterpret_cast<float2*>(smem + L::ML);
+    int base = 0, n_done = 0, n_dual = 0;
+    int done_b = 0;  // tile A's view of tile B's count (blocks of at most 128 rows)
+    bool ok = true, more = true;
+    for (int k = 0; ok && more; ++k) {
+      if (!(ok = wwait(C_PCF + k % NPC, k / NPC, 239))) break;
+      const Piece& pc = pieces[k % NPC];  // kept until the piece is done
+      const int t0 = pc.t0, t1 = pc.t1, kt = pc.kt[x], dual = pc.dual;
+      more = !pc.last;
+      int lim;
+      float f;
+      {
+        // ---- this thread's Q row as fp16, scaled by a power of two
+        const Seq s = {pc.q0, pc.m, pc.n};
+        const int hk = pc.hk, r = pc.row0 + i + (dual ? 0 : x * BM), ii = r / p.G;
+        const bool live = r < s.m * p.G;
+        lim = live ? row_limit(p, s, r) : -1;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride +
+                                                          (long long)(hk * p.G + r - ii * p.G) * D);
+        float m = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+        }
+        float inv;
+        const float sc = pow2_to_fp16(m, inv);
+        uint8_t* qt = smem + L::Q + x * L::TILE;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 hv = __floats2half2_rn(__uint_as_float(w[e] << 16) * sc, __uint_as_float(w[e] & 0xFFFF0000u) * sc);
+            h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+          }
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * L::ATOM + swz128_offset(i, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        f = p.scale_log2 * inv * (TOK ? 1.0f : __ldg(p.c.ks + hk));
+        if (f == 0.0f) f = 1e-37f;  // a zero K scale: scores vanish, and hidden keys stay at -inf
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bar[C_Q]);
+        // both warpgroups: none runs a piece ahead of the other (the merge of the two goes through ml)
+        if (!(ok = wwait(C_Q, k, 254))) break;
+      }
+      const int lim_lo = p.causal ? pc.n - pc.m + pc.row0 / p.G : pc.n - 1;  // every row of the block sees the keys up to here
+      // factors of V: 2^(x - m_run + 7), x with log2 s_v in the per-token modes; m_raw: m_run before f
+      float m_run = -INFINITY, m_raw = 0.0f, l_run = 0.0f;
+      bool first = true;
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int j = base + t - t0, ss = j % NSC;
+        const float* sc = reinterpret_cast<const float*>(smem + L::SC + ss * L::SCB);
+        if (TOK && !(ok = wwait(C_SCF + ss, j / NSC, 248))) break;
+        if (!has_tile(t0, t1, kt, dual, x, t)) {
+          if (TOK) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[C_SCE + ss]);
+          }
+          continue;
+        }
+        if (!(ok = wwait(C_SF + x, n_done, 249))) break;
+        tc_fence_after();
+        const bool masked = t * TN + TN - 1 > lim_lo;
+        // the row's 128 scores: masked, and in the per-token modes in log2 units with log2 s_v
+        float v[TN];
+        auto load_s = [&]() {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t tr[64];
+            tmem_ld32(tS + loff + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&tr[0]));
+            tmem_ld32(tS + loff + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&tr[32]));
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+              float* o = &v[64 * h + k];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = __uint_as_float(tr[k + e]);
+              if (TOK) {
+                const float4 ks = lds4(sc + 64 * h + k), lv = lds4(sc + TN + 64 * h + k);
+                attn::fmul2(o[0], o[1], ks.x, ks.y);
+                attn::fmul2(o[2], o[3], ks.z, ks.w);
+                attn::ffma2(o[0], o[1], f, f, lv.x, lv.y);
+                attn::ffma2(o[2], o[3], f, f, lv.z, lv.w);
+              }
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < TN; ++k)
+              if (t * TN + k > lim) v[k] = -INFINITY;
+          }
+        };
+        load_s();
+        // After a row's first tile the maximum rarely moves: the factors are taken against the old one, and
+        // their sum tells whether that was safe (below 2^15 every one fits fp16).  Otherwise, and on a row's first
+        // tile, the tile's maximum is taken first, and O rescaled if it moves.
+        float l_tile = 0.0f;
+        bool exact = __any_sync(0xffffffffu, m_run == -INFINITY);
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          if (exact) {
+            float mx[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              mx[e] = v[e];
+#pragma unroll
+              for (int q = 1; q < TN / 8; q += 2)
+                mx[e] = q + 1 < TN / 8 ? attn::fmax3(mx[e], v[e + 8 * q], v[e + 8 * q + 8]) : fmaxf(mx[e], v[e + 8 * q]);
+            }
+            const float mt = attn::fmax3(attn::fmax3(mx[0], mx[1], mx[2]), attn::fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            const float mts = TOK || mt == -INFINITY ? mt : mt * f;
+            const float m_new = mts > m_run + 8.0f ? mts : m_run;
+            const float alpha = m_new == m_run ? 1.0f : attn::ex2(m_run - m_new);  // 0 from -inf
+            if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
+              if (!(ok = wwait(C_PV + x, n_done - 1, 250))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tO + loff + c * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16(tO + loff + c * 16, o);
+              }
+              tmem_st_wait();
+            }
+            l_run *= alpha;
+            if (m_new != m_run) m_raw = mt;
+            m_run = m_new;
+          }
+          // scores past 2^20: v f and the rounded maximum would differ by more than an exponent can bear, so
+          // the maximum is taken off before f
+          const bool far = !TOK && __any_sync(0xffffffffu, m_run > -INFINITY && fabsf(m_run) > 0x1p20f);
+          const float nb = m_run == -INFINITY ? 0.0f : kShift - (far ? 0.0f : m_run);
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (far) {
+#pragma unroll
+            for (int k = 0; k < TN; ++k) v[k] -= m_raw;
+          }
+#pragma unroll
+          for (int k = 0; k < TN; k += 4) {
+            if (TOK) {
+              attn::fadd2(v[k], v[k + 1], nb, nb);
+              attn::fadd2(v[k + 2], v[k + 3], nb, nb);
+            } else {
+              attn::ffma2(v[k], v[k + 1], f, f, nb, nb);
+              attn::ffma2(v[k + 2], v[k + 3], f, f, nb, nb);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[k + e] = attn::ex2(v[k + e]);
+            attn::fadd2(ls[0], ls[1], v[k], v[k + 1]);
+            attn::fadd2(ls[2], ls[3], v[k + 2], v[k + 3]);
+            if (TOK) {
+              const float4 iv = lds4(sc + 2 * TN + k);
+              // in place (volatile): the compiler would put these off, and spill the factors meanwhile
+              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[0]) : "f"(v[k]), "f"(iv.x));
+              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[1]) : "f"(v[k + 1]), "f"(iv.y));
+              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[2]) : "f"(v[k + 2]), "f"(iv.z));
+              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[3]) : "f"(v[k + 3]), "f"(iv.w));
+            }
+          }
+          const float w = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          l_tile = TOK ? (lp[0] + lp[1]) + (lp[2] + lp[3]) : w;
+          if (exact || !__any_sync(0xffffffffu, !(w < 32768.0f))) break;
+          exact = true;
+          load_s();
+        }
+        if (!ok) break;
+        // ---- P: the factors as fp16, over S
+        uint32_t hp[TN / 2];
+#pragma unroll
+        for (int k = 0; k < TN; k += 2) {
+          const __half2 hv = __floats2half2_rn(v[k], v[k + 1]);
+          hp[k / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        tmem_st32(tS + loff, *reinterpret_cast<uint32_t(*)[32]>(&hp[0]));
+        tmem_st32(tS + loff + 32, *reinterpret_cast<uint32_t(*)[32]>(&hp[32]));
+        tmem_st_wait();
+        l_run += l_tile;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar[C_PF + x]);
+          if (TOK) mbar_arrive(&bar[C_SCE + ss]);
+        }
+        ++n_done;
+        first = false;
+      }
+      base += t1 - t0;
+      if (!ok) break;
+      // -------------------------------------------------------------- results
+      const bool any = tile_count(t0, t1, kt, dual, x) > 0;
+      const int n_b = tile_count(t0, t1, pc.kt[1], dual, 1);
+      if (any && !(ok = wwait(C_PV + x, n_done - 1, 251))) break;
+      tc_fence_after();
+      float m_ref = m_run == -INFINITY ? -INFINITY : m_run - kShift;  // l and O are in units of 2^m_ref
+      float wa = 1.0f, wb = 0.0f;
+      if (dual) {
+        if (x == 1) {
+          ml[i] = make_float2(m_ref, l_run);
+          mbar_arrive(&bar[C_ML]);
+        } else {
+          if (!(ok = wwait(C_ML, n_dual, 252))) break;
+          done_b += n_b;
+          if (n_b > 0 && !(ok = wwait(C_PV + 1, done_b - 1, 253))) break;
+          tc_fence_after();
+          const float2 o = ml[i];
+          const float m = fmaxf(m_ref, o.x);
+          wa = m_ref == -INFINITY ? 0.0f : attn::ex2(m_ref - m);
+          wb = o.x == -INFINITY ? 0.0f : attn::ex2(o.x - m);
+          l_run = l_run * wa + o.y * wb;
+          m_ref = m;
+        }
+        ++n_dual;
+      } else {
+        done_b += n_b;
+      }
+      if (!(dual && x == 1)) {
+        const bool any_b = dual && n_b > 0;
+        const bool whole = pc.whole;
+        const int hk = pc.hk, r = pc.row0 + i + (dual ? 0 : x * BM), ii = r / p.G;
+        const bool live = r < pc.m * p.G;
+        const long long slot_row = (long long)pc.slot * PL::RB + (r - pc.row0);
+        const long long out_row = (long long)(pc.q0 + ii) * p.Hq + hk * p.G + r - ii * p.G;
+        const float fac = whole ? row_factor(p, hk, l_run, m_ref, m_ref) : 1.0f;
+        if (live) {
+          if (whole) {
+            if (p.lse) p.lse[out_row] = row_lse(l_run, m_ref);
+          } else {
+            p.part_ml[slot_row] = make_float4(m_ref, l_run, m_ref, 0.0f);
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16], ob[16];
+          if (any) tmem_ld16(tO + loff + c * 16, o);
+          if (any_b) tmem_ld16(tbase + L::TO1 + loff + c * 16, ob);
+          tmem_ld_wait();
+          float y[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            y[k] = any && wa != 0.0f ? __uint_as_float(o[k]) * wa : 0.0f;
+            if (any_b && wb != 0.0f) y[k] += __uint_as_float(ob[k]) * wb;
+            y[k] *= fac;
+          }
+          if (live && whole) {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const __nv_bfloat162 v2 = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+              h[e] = *reinterpret_cast<const uint32_t*>(&v2);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c * 16);
+            dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          } else if (live) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + slot_row * D + c * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C_PCE + k % NPC]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D, bool FP8, bool TOK, bool ALL>
+cudaError_t launch_a(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int grid, cudaStream_t s) {
+  auto kern = paged_chunk_kernel<D, FP8, TOK, ALL>;
+  cudaError_t e;
+  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), CL<D>::ALLOC)) != cudaSuccess) return e;
+  kern<<<grid, CT, CL<D>::ALLOC, s>>>(mk, mv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  combine_kernel<CPL<ALL>, D><<<dim3(grid, 8), 128, 0, s>>>(p, grid);
+  return cudaGetLastError();
+}
+
+template <int D, bool ALL>
+cudaError_t launch_mode(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int mode, int grid, cudaStream_t s) {
+  switch (mode) {
+    case FA_MODE_INT8_PER_HEAD: return launch_a<D, false, false, ALL>(mk, mv, p, grid, s);
+    case FA_MODE_FP8_PER_HEAD: return launch_a<D, true, false, ALL>(mk, mv, p, grid, s);
+    case FA_MODE_INT8_PER_TOKEN: return launch_a<D, false, true, ALL>(mk, mv, p, grid, s);
+    case FA_MODE_FP8_PER_TOKEN: return launch_a<D, true, true, ALL>(mk, mv, p, grid, s);
+    default: return cudaErrorNotSupported;
+  }
+}
+
+}  // namespace
+
+size_t paged_chunk_ws(int D) { return plan_ws<CPL<false>>(D, sm_count()); }
+
+cudaError_t launch_paged_chunk(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
+  AttnP p = paged_attn_params(a);
+  const int D = a.q->D, grid = sm_count();
+  plan_carve<CPL<false>>(p, ws, D, grid);
+  CUtensorMap mk, mv;
+  cudaError_t e;
+  if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, UR, false)) != cudaSuccess) return e;
+  if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, UR, false)) != cudaSuccess) return e;
+  return D == 128 ? launch_mode<128, false>(mk, mv, p, a.cache->mode, grid, s)
+                  : launch_mode<64, true>(mk, mv, p, a.cache->mode, grid, s);
+}
+
+}  // namespace faq

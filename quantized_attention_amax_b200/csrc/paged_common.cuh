@@ -24,6 +24,7 @@ struct Cache {
   int head_stride, tok_stride;
   int pages, H, page_shift, page_mask;
   int per_token;  // scales [pages, H, page_size], else [H]
+  int bnsd;       // pages are [H, page_size, D], else [page_size, H, D]
 
   __device__ __forceinline__ long long row(int pg, int h, int slot) const {
     return (long long)pg * page_stride + (long long)h * head_stride + (long long)slot * tok_stride;
@@ -140,6 +141,7 @@ inline paged::Cache paged_cache_of(const fa_paged_cache& c) {
   o.H = c.H;
   while ((1 << o.page_shift) < c.page_size) ++o.page_shift;
   o.page_mask = c.page_size - 1;
+  o.bnsd = bnsd;
   o.per_token = c.mode == FA_MODE_INT8_PER_TOKEN || c.mode == FA_MODE_FP8_PER_TOKEN;
   return o;
 }

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(DT, 2)
     // ------------------------------------------------------------------ loads
     // a tile is 128 / page boxes (one for pages of 128 keys and more): lane l loads box l's K and V
     const int box = min(TK, p.c.page_mask + 1), nbox = TK / box;
-    const bool bnsd = p.c.tok_stride == HD;
+    const bool bnsd = p.c.bnsd;
     if (lane == 0) {
       tma_prefetch_desc(&tmk);
       tma_prefetch_desc(&tmv);
@@ -533,8 +533,8 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, int rows, void* ws, cuda
   plan_carve<DPL>(p, ws, HD, grid);
   CUtensorMap mk, mv;
   cudaError_t e;
-  if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, TK)) != cudaSuccess) return e;
-  if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, TK)) != cudaSuccess) return e;
+  if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, TK, true)) != cudaSuccess) return e;
+  if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, TK, true)) != cudaSuccess) return e;
   switch (a.cache->mode) {
     case FA_MODE_INT8_PER_HEAD: return launch_mode<false, false>(mk, mv, p, rows, grid, s);
     case FA_MODE_FP8_PER_HEAD: return launch_mode<true, false>(mk, mv, p, rows, grid, s);

@@ -28,41 +28,82 @@ struct AttnP {
   int* status;
 };
 
-// Sequences whose row count lies in [MINR, MAXR] are this kernel's.
-template <int UK_, int RB_, int MINR_, int MAXR_>
+// Sequences whose row count lies in [MINR, MAXR] are this kernel's.  TRIM: causal row blocks count only the
+// units they see (worth it where blocks are many; their sums have no closed form).
+template <int UK_, int RB_, int MINR_, int MAXR_, bool TRIM_ = false>
 struct Plan {
   static constexpr int UK = UK_, RB = RB_, MINR = MINR_, MAXR = MAXR_;
+  static constexpr bool TRIM = TRIM_;
 };
 
 struct Item {
   int b, hk, rb;    // sequence, kv head, row block
   Seq s;
-  int nrb, nt;      // the sequence's row blocks, units of each
+  int nrb, nt;      // the sequence's row blocks, units of this one
   long long first;  // first unit of the item
 };
 
+// Sequence b and its row blocks (none if it is not this plan's).
 template <typename PL>
-__device__ __forceinline__ void seq_units(const AttnP& p, int b, Seq& s, int& nrb, int& nt) {
+__device__ __forceinline__ void seq_blocks(const AttnP& p, int b, Seq& s, int& nrb) {
   s = load_seq(p.bt, p.c.page_shift, b, p.status, 211);
   const long long rows = (long long)s.m * p.G;
-  const bool mine = rows >= PL::MINR && rows <= PL::MAXR;
-  nrb = mine ? (int)((rows + PL::RB - 1) / PL::RB) : 0;
-  nt = mine ? max(1, (s.n + PL::UK - 1) / PL::UK) : 0;  // a sequence without keys still has rows to write
+  nrb = rows >= PL::MINR && rows <= PL::MAXR ? (int)((rows + PL::RB - 1) / PL::RB) : 0;
+}
+
+// Units of row block rb: at least one, since rows that see no key are written too.
+template <typename PL>
+__device__ __forceinline__ int block_units(const AttnP& p, const Seq& s, int rb) {
+  int end = s.n;
+  if (PL::TRIM && p.causal) {
+    const int last = min((rb + 1) * PL::RB, s.m * p.G) - 1;
+    end = min(s.n, s.n - s.m + last / p.G + 1);
+  }
+  return max(1, (end + PL::UK - 1) / PL::UK);
+}
+
+// Units of one kv head of each lane's sequence (a warp's work).
+template <typename PL>
+__device__ __forceinline__ long long head_units(const AttnP& p, const Seq& s, int nrb, int lane) {
+  if (!PL::TRIM || !p.causal) return nrb ? (long long)nrb * block_units<PL>(p, s, 0) : 0;
+  long long w = 0;
+  if (nrb <= 4)
+    for (int k = 0; k < nrb; ++k) w += block_units<PL>(p, s, k);
+  for (unsigned big = __ballot_sync(0xffffffffu, nrb > 4); big; big &= big - 1) {
+    const int src = __ffs(big) - 1;
+    const Seq o = {0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src)};
+    const int no = __shfl_sync(0xffffffffu, nrb, src);
+    long long v = 0;
+    for (int k = lane; k < no; k += 32) v += block_units<PL>(p, o, k);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == src) w = v;
+  }
+  return w;
 }
 
 // All units of the batch (every lane of the warp gets the sum).
 template <typename PL>
 __device__ __forceinline__ long long total_units(const AttnP& p, int lane) {
   long long w = 0;
-  for (int b = lane; b < p.bt.B; b += 32) {
-    Seq s;
-    int nrb, nt;
-    seq_units<PL>(p, b, s, nrb, nt);
-    w += (long long)nrb * nt;
+  for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
+    Seq s = {0, 0, 0};
+    int nrb = 0;
+    if (b0 + lane < p.bt.B) seq_blocks<PL>(p, b0 + lane, s, nrb);
+    w += head_units<PL>(p, s, nrb, lane);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
   return w * p.c.H;
+}
+
+__device__ __forceinline__ long long lanes_before(long long v, int lane) {  // sum over the lanes up to this one
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += o;
+  }
+  return v;
 }
 
 // The item that holds unit u < total (a warp's work).
@@ -71,34 +112,44 @@ __device__ __forceinline__ Item find_item(const AttnP& p, long long u, int lane)
   long long base = 0;
   Item it = {};
   for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
-    const int b = b0 + lane;
     Seq s = {0, 0, 0};
-    int nrb = 0, nt = 0;
-    if (b < p.bt.B) seq_units<PL>(p, b, s, nrb, nt);
-    const long long mine = (long long)nrb * nt * p.c.H;
-    long long end = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, end, off);
-      if (lane >= off) end += o;
+    int nrb = 0;
+    if (b0 + lane < p.bt.B) seq_blocks<PL>(p, b0 + lane, s, nrb);
+    const long long head = head_units<PL>(p, s, nrb, lane), mine = head * p.c.H;
+    const long long end = base + lanes_before(mine, lane);
+    const unsigned after = __ballot_sync(0xffffffffu, end > u);
+    if (!after) {
+      base = __shfl_sync(0xffffffffu, end, 31);
+      continue;
     }
-    const unsigned after = __ballot_sync(0xffffffffu, base + end > u);
-    if (after) {
-      const int src = __ffs(after) - 1;
-      it.b = b0 + src;
-      it.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-      it.s.m = __shfl_sync(0xffffffffu, s.m, src);
-      it.s.n = __shfl_sync(0xffffffffu, s.n, src);
-      it.nrb = __shfl_sync(0xffffffffu, nrb, src);
-      it.nt = __shfl_sync(0xffffffffu, nt, src);
-      const long long start = base + __shfl_sync(0xffffffffu, end - mine, src);
-      const long long k = (u - start) / it.nt;  // (hk, rb) of the unit
-      it.hk = (int)(k / it.nrb);
-      it.rb = (int)(k - (long long)it.hk * it.nrb);
-      it.first = start + k * it.nt;
+    const int src = __ffs(after) - 1;
+    it.b = b0 + src;
+    it.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+    it.s.m = __shfl_sync(0xffffffffu, s.m, src);
+    it.s.n = __shfl_sync(0xffffffffu, s.n, src);
+    it.nrb = __shfl_sync(0xffffffffu, nrb, src);
+    const long long start = __shfl_sync(0xffffffffu, end - mine, src), per = __shfl_sync(0xffffffffu, head, src);
+    it.hk = (int)((u - start) / per);
+    it.first = start + it.hk * per;
+    if (!PL::TRIM || !p.causal) {
+      it.nt = block_units<PL>(p, it.s, 0);
+      it.rb = (int)((u - it.first) / it.nt);
+      it.first += (long long)it.rb * it.nt;
       return it;
     }
-    base += __shfl_sync(0xffffffffu, end, 31);
+    for (int k0 = 0; k0 < it.nrb; k0 += 32) {
+      const int n = k0 + lane < it.nrb ? block_units<PL>(p, it.s, k0 + lane) : 0;
+      const long long e = it.first + lanes_before(n, lane);
+      const unsigned in = __ballot_sync(0xffffffffu, e > u);
+      if (in) {
+        const int k = __ffs(in) - 1;
+        it.rb = k0 + k;
+        it.nt = __shfl_sync(0xffffffffu, n, k);
+        it.first = __shfl_sync(0xffffffffu, e, k) - it.nt;
+        return it;
+      }
+      it.first = __shfl_sync(0xffffffffu, e, 31);
+    }
   }
   it.b = p.bt.B;
   return it;
@@ -108,14 +159,17 @@ __device__ __forceinline__ Item find_item(const AttnP& p, long long u, int lane)
 template <typename PL>
 __device__ __forceinline__ bool next_item(const AttnP& p, Item& it) {
   it.first += it.nt;
-  if (++it.rb < it.nrb) return true;
-  it.rb = 0;
-  if (++it.hk < p.c.H) return true;
-  it.hk = 0;
-  do {
-    if (++it.b >= p.bt.B) return false;
-    seq_units<PL>(p, it.b, it.s, it.nrb, it.nt);
-  } while (it.nt == 0);
+  if (++it.rb == it.nrb) {
+    it.rb = 0;
+    if (++it.hk == p.c.H) {
+      it.hk = 0;
+      do {
+        if (++it.b >= p.bt.B) return false;
+        seq_blocks<PL>(p, it.b, it.s, it.nrb);
+      } while (it.nrb == 0);
+    }
+  }
+  it.nt = block_units<PL>(p, it.s, it.rb);
   return true;
 }
 
@@ -219,12 +273,24 @@ inline paged::AttnP paged_attn_params(const PagedAttnArgs& a) {
   return p;
 }
 
-// Tensor map over a cache's codes: boxes of one page's (at most `keys`) rows of one head, 128-byte
-// rows with the 128-byte swizzle (64-byte rows: the 64-byte one).  A page index past the pool reads zeros.
-inline cudaError_t make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache& c, int keys) {
-  const int rows = c.page_size < keys ? c.page_size : keys;
-  // the layouts' [pages, H, page, D] and [pages, page, H, D] are those of a [B, H, S, D] tensor
-  return attn::make_code_map(map, base, c.pages, c.H, c.page_size, c.D, c.layout, rows);
+// Tensor map over a cache's codes: boxes of one page's (at most `keys`) rows of one head, with the swizzle of
+// MMA operands of that row length (128 or 64 bytes) or rows one behind the other.  A page index past the pool
+// reads zeros.
+inline cudaError_t make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache& c, int keys, bool swizzle) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const bool bnsd = c.layout == FA_LAYOUT_BNSD;
+  const cuuint64_t D = c.D, H = c.H, P = c.page_size;
+  const cuuint32_t rows = c.page_size < keys ? c.page_size : keys;
+  const cuuint64_t dims[4] = {D, bnsd ? P : H, bnsd ? H : P, (cuuint64_t)c.pages};
+  const cuuint64_t strides[3] = {D, (bnsd ? P : H) * D, H * P * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, bnsd ? rows : 1, bnsd ? 1 : rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle swz = !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace faq

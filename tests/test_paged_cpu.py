@@ -31,7 +31,7 @@ def rows(N, T=5, H=4, D=128, stride=None, data=0x80000):
 
 
 BAD_CACHES = [(dict(mode=0), UNSUPPORTED), (dict(mode=3), UNSUPPORTED), (dict(mode=4), UNSUPPORTED),
-              (dict(mode=7), UNSUPPORTED), (dict(mode=9), UNSUPPORTED), (dict(H=0), INVALID), (dict(pages=-1), INVALID),
+              (dict(mode=7), UNSUPPORTED), (dict(mode=9), UNSUPPORTED), (dict(H=0), INVALID), (dict(pages=0), INVALID), (dict(pages=-1), INVALID),
               (dict(D=96), UNSUPPORTED), (dict(page=8), UNSUPPORTED), (dict(page=48), UNSUPPORTED),
               (dict(page=2048), UNSUPPORTED), (dict(layout=2), INVALID), (dict(k=0x10008), INVALID),
               (dict(v=None), INVALID), (dict(ks=None), INVALID), (dict(vs=0x40002), INVALID),

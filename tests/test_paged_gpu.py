@@ -67,6 +67,8 @@ SHAPES = [
     ((400,), (150,), 10, 2, 128, 1024),
     ((129, 1, 640), (1, 1, 17), 34, 2, 128, 64),
     ((1500, 1100), (260, 1), 8, 1, 128, 64),
+    ((700, 130, 16), (1, 1, 1), 5, 1, 128, 16),
+    ((90, 33), (2, 1), 3, 1, 64, 16),
 ]
 
 
@@ -586,5 +588,6 @@ def test_tensors_of_another_kind_are_refused(faq):
         faq.paged_evict(c, b, torch.zeros(1, 2, 32).cuda(), 4, 3, 2)
     assert e.value.status == 1
     with pytest.raises(faq.FaqError) as e:
-        faq.paged_attention(q, c, b, workspace=torch.empty(1 << 24, dtype=torch.uint8).cuda()[1:])
+        need = faq.paged_attention_workspace_size(q, c, b)
+        faq.paged_attention(q, c, b, workspace=torch.empty(need + 1, dtype=torch.uint8).cuda()[1:])
     assert e.value.status == 7

@@ -13,9 +13,9 @@
 // largest).  TMA brings the codes page by page to a staging ring, four warps convert them and write the swizzled
 // MMA operands (about 2000 warp instructions a tile, which fit beside the softmax of 256 rows: the cache needs
 // no conversion pass of its own).  P (fp16, up to 2^15) overwrites S in TMEM and is the A operand of
-// P V.  Scales: per head at the ends.  Per token: s_k on the scores, and s_v in the exponent, so that a row's
-// factors p s_v are held against the largest of them, whatever the scales' range:
-//   w_j = 2^(x_j + log2 s_v(j) - mv), mv the running maximum of x + log2 s_v;  sum p = 2^mv sum w_j / s_v(j).
+// P V.  Scales: per head at the ends.  Per token: s_k on the scores, s_v on P; a row's factors are held against
+// the largest of them, whatever the scales' range: w_j = s_v(j) 2^(x_j - mv), mv the running maximum of
+// x + log2 s_v, and the sum of p is that of 2^(x_j - mv).
 // Work is shared out as paged_sched.cuh says: a causal block counts the key tiles it sees.
 #include "paged_sched.cuh"
 
@@ -28,13 +28,12 @@ constexpr int TN = 128;       // keys per tile
 constexpr int NSG = 2;        // K and V stages
 constexpr int NSC = 3;        // scale stages (per-token modes)
 constexpr int CT = 512;       // warpgroups: pieces + loads, MMAs; converters; softmax A; softmax B
-constexpr int UR = 32;        // keys of a load unit
-constexpr int NU = 6;         // units in the staging ring
-constexpr int R0 = 56, RC = 72, RS = 192;  // the warpgroups' registers
+constexpr int NU = 3;         // load units in the staging ring (one is converted, two are on their way)
+constexpr int R0 = 88, RC = 88, RS = 168;  // the warpgroups' registers
 static_assert(128 * (R0 + RC + 2 * RS) <= CT * 128, "register split exceeds the launch");
 static_assert(R0 <= 128 && RC <= 128 && RS >= 128, "launched with 128 registers a thread: the first two warpgroups give some back");
 constexpr float kShift = 7.0f;  // P is held as p 2^7: fp16 keeps 11 bits of it down to 2^-21, and the running maximum may lag by 2^8
-// V scales below this are brought up to it, and their codes (exact otherwise) scaled down: 1 / s_v stays finite
+// V scales below this are brought up to it, and their codes (exact otherwise) scaled down: 2^(x - mv) stays finite
 constexpr float kMinScale = 0x1p-90f;
 
 template <bool ALL>
@@ -48,12 +47,14 @@ struct CL {
   static constexpr uint32_t Q = 0;                     // two tiles
   static constexpr uint32_t K = Q + 2 * TILE;          // NSG stages
   static constexpr uint32_t V = K + NSG * TILE;        // NSG stages
-  static constexpr uint32_t SC = V + NSG * TILE;       // NSC x ([128] s_k, [128] log2 s_v, [128] 1 / s_v, [128] factors of V)
-  static constexpr uint32_t SCB = 4 * TN * 4;
+  static constexpr uint32_t SC = V + NSG * TILE;       // NSC x ([128] s_k, [128] s_v, [128] factors of V codes, [4] warps that have one, [4] largest s_v)
+  static constexpr uint32_t SCB = 3 * TN * 4 + 64;
   static constexpr uint32_t ML = SC + NSC * SCB;       // [128] (m, l) of tile B (blocks of at most 128 rows)
   static constexpr uint32_t PC = ML + BM * 8;          // NPC pieces
   static constexpr uint32_t BAR = PC + 4 * 64;
-  static constexpr uint32_t UNIT = UR * D;             // raw codes
+  static constexpr int UR = 8192 / D;                  // keys of a load unit
+  static constexpr int UT = TN / UR;                   // units of a tile of one operand
+  static constexpr uint32_t UNIT = UR * D;             // raw codes: 8 KB
   static constexpr uint32_t RAW = (BAR + 384 + 127) & ~127u;  // NU units on their way
   static constexpr uint32_t TOTAL = RAW + NU * UNIT;
   static constexpr uint32_t ALLOC = TOTAL + 1024;
@@ -94,6 +95,11 @@ __device__ __forceinline__ float4 lds4(const float* p) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(p)) : "memory");
   return v;
 }
+
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
+};
 
 // One piece of the CTA's run: key tiles [t0, t1) of a row block.  Warp 0 walks the run and leaves the
 // pieces in a ring in shared memory, so that the other warps spend no registers on the walk.
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(CT, 1)
       // ------------------------------------------ the run's pieces, and their loads
       const long long u0 = run_start(total, blockIdx.x, runs), u1 = run_start(total, blockIdx.x + 1, runs);
       Item it = find_item<PL>(p, u0, lane);
-      const int box = min(UR, p.c.page_mask + 1), nbox = UR / box;  // a unit is one box, or two of 16-key pages
+      const int box = min(L::UR, p.c.page_mask + 1), nbox = L::UR / box;  // lane l < nbox loads a unit's l-th box
       const bool bnsd = p.c.bnsd;
       if (lane == 0) {
         tma_prefetch_desc(&tmk);
@@ -240,15 +246,15 @@ __global__ void __launch_bounds__(CT, 1)
         for (int t = pc.t0; t < pc.t1 && ok; ++t) {
           const int next = page(t + 1);  // its latency passes while this tile's units wait
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q, ++g) {
-            const int sl = g % NU, row = (q & 3) * UR + lane * box;  // this lane's box
+          for (int q = 0; q < 2 * L::UT; ++q, ++g) {
+            const int sl = g % NU, row = (q % L::UT) * L::UR + lane * box;  // this lane's box
             const int pg = __shfl_sync(0xffffffffu, pages, (row >> 4) & 7);
             if (g >= NU && !(ok = wwait(C_RE + sl, g / NU - 1, 238))) break;
             if (lane == 0) mbar_arrive_expect_tx(&bar[C_RF + sl], L::UNIT);
             __syncwarp();
             if (lane < nbox) {
               const int off = (t * TN + row) & p.c.page_mask;
-              tma_load_4d(smem + L::RAW + sl * L::UNIT + lane * box * D, q < 4 ? &tmk : &tmv, &bar[C_RF + sl], 0,
+              tma_load_4d(smem + L::RAW + sl * L::UNIT + lane * box * D, q < L::UT ? &tmk : &tmv, &bar[C_RF + sl], 0,
                           bnsd ? off : pc.hk, bnsd ? pc.hk : off, pg);
             }
           }
@@ -330,8 +336,9 @@ __global__ void __launch_bounds__(CT, 1)
   } else if (warp < 8) {
     regs_dec<RC>();
     // ------------------------------------------- codes -> fp16 operand tiles
-    // A tile comes in eight units of 32 keys (four of K, four of V).  Thread: chunk c (16 codes, 32 bytes of fp16; D / 16
-    // lanes a row) of every RPP-th row.  Its key's scales come a tile ahead.
+    // A tile comes in 2 UT units, K first.  Thread: chunk c (16 codes, 32 bytes of fp16; D / 16 lanes a row) of every
+    // RPP-th row.  Its key's scales come a tile ahead.
+    constexpr int UT = L::UT, UR = L::UR;
     constexpr int LPR = D / 16, RPP = 128 / LPR, NP = UR / RPP;  // lanes per row, rows per pass, passes per unit
     const int ct = tid - 128, c = ct % LPR, r0 = ct / LPR;
     // the two 16-byte chunks of a row: lanes of the row's halves (D = 64: of odd rows) write them in turn, so that
@@ -372,8 +379,8 @@ __global__ void __launch_bounds__(CT, 1)
         const int j = base + t - t0, st = j % NSG, ss = j % NSC;
         float* sc = reinterpret_cast<float*>(smem + L::SC + ss * L::SCB);
         if (TOK) {
-          // s_k, log2 s_v, 1 / s_v and the factor of the V codes (1 but for tiny scales).  A NaN or infinite
-          // s_v is given to the rows that see the key by s_k.
+          // s_k, s_v and the factor of the V codes (1 but for tiny scales).  A NaN or infinite s_v is given to
+          // the rows that see the key by s_k.
           float f = 1.0f;
           if (!(fabsf(sv) < INFINITY)) {
             sk = __uint_as_float(0x7FC00000u);
@@ -385,11 +392,15 @@ __global__ void __launch_bounds__(CT, 1)
           }
           if (j >= NSC && !(ok = wwait(C_SCE + ss, j / NSC - 1, 245))) break;
           sc[ct] = sk;
-          sc[TN + ct] = log2f(sv);
-          sc[2 * TN + ct] = 1.0f / sv;
-          sc[3 * TN + ct] = f;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[C_SCF + ss]);
+          sc[TN + ct] = sv;
+          sc[2 * TN + ct] = f;
+          const bool any_f = __any_sync(0xffffffffu, f != 1.0f);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sv));
+          if (lane == 0) {
+            sc[3 * TN + (warp & 3)] = any_f ? 1.0f : 0.0f;
+            sc[3 * TN + 4 + (warp & 3)] = __uint_as_float(top);
+            mbar_arrive(&bar[C_SCF + ss]);
+          }
           load_scales(t + 1, raw_page);
           raw_page = load_page(t + 2);
         }
@@ -398,19 +409,19 @@ __global__ void __launch_bounds__(CT, 1)
         const bool edge = FP8 && t * TN + TN - 1 > lim_lo;
         uint32_t clear = 0;  // bit NP u + q: pass q of unit u's rows
 #pragma unroll 1
-        for (int u = 0; u < 8; ++u, ++g) {
+        for (int u = 0; u < 2 * UT; ++u, ++g) {
           const int sl = g % NU;
           if (!(ok = wwait(C_RF + sl, g / NU, 237))) break;
           if (u == 0 && j >= NSG && !(ok = wwait(C_KE + st, j / NSG - 1, 246))) break;
-          if (u == 4 && j >= NSG && !(ok = wwait(C_VE + st, j / NSG - 1, 247))) break;
-          if (u == 4 && TOK && !(ok = wwait(C_SCF + ss, j / NSC, 255))) break;  // the other warps' factors
+          if (u == UT && j >= NSG && !(ok = wwait(C_VE + st, j / NSG - 1, 247))) break;
+          if (u == UT && TOK && !(ok = wwait(C_SCF + ss, j / NSC, 255))) break;  // the other warps' factors
           uint32_t k_nan = 0;
-          if (edge && u < 4) {
-            static_assert(NU > 4, "unit u + 4 is in the ring while unit u is converted");
-            if (!(ok = wwait(C_RF + (g + 4) % NU, (g + 4) / NU, 236))) break;
+          if (edge && u < UT) {
+            static_assert(NU > UT, "unit u + UT is in the ring while unit u is converted");
+            if (!(ok = wwait(C_RF + (g + UT) % NU, (g + UT) / NU, 236))) break;
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(smem + L::RAW + ((g + 4) % NU) * L::UNIT + q * 2048 + ct * 16);
+              const uint4 x = *reinterpret_cast<const uint4*>(smem + L::RAW + ((g + UT) % NU) * L::UNIT + q * 2048 + ct * 16);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
               bool nan = false;
 #pragma unroll
@@ -422,40 +433,45 @@ __global__ void __launch_bounds__(CT, 1)
               if (row_nan && !past) k_nan |= 1u << q;
             }
           }
-          uint8_t* tile = smem + (u < 4 ? L::K : L::V) + st * L::TILE + (u & 3) * UR * 128;
+          uint8_t* tile = smem + (u < UT ? L::K : L::V) + st * L::TILE + (u % UT) * UR * 128;
           const uint8_t* raw = smem + L::RAW + sl * L::UNIT + ct * 16;
+          bool scaled = false;
+          if (TOK && u >= UT) {
+            const float4 y = *reinterpret_cast<const float4*>(sc + 3 * TN);
+            scaled = y.x + y.y + y.z + y.w != 0.0f;
+          }
+          uint4 xs[NP];
+#pragma unroll
+          for (int q = 0; q < NP; ++q) xs[q] = *reinterpret_cast<const uint4*>(raw + q * 2048);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C_RE + sl]);
 #pragma unroll
           for (int q = 0; q < NP; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4*>(raw + q * 2048);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t w[4] = {xs[q].x, xs[q].y, xs[q].z, xs[q].w};
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) codes4_to_h2<FP8>(w[e], h[2 * e], h[2 * e + 1]);
             if (FP8 && edge) {
-              const bool zero = u >= 4 && ((clear >> (NP * (u - 4) + q)) & 1u), nan = (k_nan >> q) & 1u;
+              const bool zero = u >= UT && ((clear >> (NP * (u - UT) + q)) & 1u), nan = (k_nan >> q) & 1u;
 #pragma unroll
               for (int e = 0; e < 8; ++e) h[e] = zero ? 0u : nan ? 0x7FFF7FFFu : h[e];
             }
-            if (TOK && u >= 4) {
-              const float f = sc[3 * TN + (u - 4) * UR + r0 + q * RPP];
-              if (f != 1.0f) {
-                const __half2 f2 = __float2half2_rn(f);
+            if (scaled) {
+              const __half2 f2 = __float2half2_rn(sc[2 * TN + (u - UT) * UR + r0 + q * RPP]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), f2);
-                  h[e] = *reinterpret_cast<const uint32_t*>(&y);
-                }
+              for (int e = 0; e < 8; ++e) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), f2);
+                h[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
             }
             const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
             *reinterpret_cast<uint4*>(tile + at0 + q * RPP * 128) = odd ? hi : lo;
             *reinterpret_cast<uint4*>(tile + at1 + q * RPP * 128) = odd ? lo : hi;
           }
-          if ((u & 3) == 3) fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar[C_RE + sl]);
-            if ((u & 3) == 3) mbar_arrive(&bar[(u < 4 ? C_KF : C_VF) + st]);
+          if (u % UT == UT - 1) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[(u < UT ? C_KF : C_VF) + st]);
           }
         }
       }
@@ -521,7 +537,8 @@ __global__ void __launch_bounds__(CT, 1)
         if (!(ok = wwait(C_Q, k, 254))) break;
       }
       const int lim_lo = p.causal ? pc.n - pc.m + pc.row0 / p.G : pc.n - 1;  // every row of the block sees the keys up to here
-      // factors of V: 2^(x - m_run + 7), x with log2 s_v in the per-token modes; m_raw: m_run before f
+      // factors of V: 2^(x - m_run + 7), times s_v in the per-token modes, whose m_run is that of x + log2 s_v;
+      // m_raw: m_run before f
       float m_run = -INFINITY, m_raw = 0.0f, l_run = 0.0f;
       bool first = true;
       for (int t = t0; t < t1 && ok; ++t) {
@@ -538,52 +555,67 @@ __global__ void __launch_bounds__(CT, 1)
         if (!(ok = wwait(C_SF + x, n_done, 249))) break;
         tc_fence_after();
         const bool masked = t * TN + TN - 1 > lim_lo;
-        // the row's 128 scores: masked, and in the per-token modes in log2 units with log2 s_v
-        float v[TN];
-        auto load_s = [&]() {
+        // The row's scores, CW at a time (all 128 at once spill), times s_k in the per-token modes, masked.
+        constexpr int CW = 64;
+        auto scores = [&](auto&& use, auto fresh) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t tr[64];
-            tmem_ld32(tS + loff + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&tr[0]));
-            tmem_ld32(tS + loff + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&tr[32]));
+          for (int c = 0; c < TN; c += CW) {
+            uint32_t tr[CW];
+#pragma unroll
+            for (int q = 0; q < CW; q += 32) tmem_ld32(tS + loff + c + q, *reinterpret_cast<uint32_t(*)[32]>(&tr[q]));
             tmem_ld_wait();
+            float v[CW];
 #pragma unroll
-            for (int k = 0; k < 64; k += 4) {
-              float* o = &v[64 * h + k];
+            for (int k = 0; k < CW; ++k) v[k] = __uint_as_float(tr[k]);
+            if (TOK) {
+              // the scales of 16 keys at a time: their loads' latencies pass together
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = __uint_as_float(tr[k + e]);
-              if (TOK) {
-                const float4 ks = lds4(sc + 64 * h + k), lv = lds4(sc + TN + 64 * h + k);
-                attn::fmul2(o[0], o[1], ks.x, ks.y);
-                attn::fmul2(o[2], o[3], ks.z, ks.w);
-                attn::ffma2(o[0], o[1], f, f, lv.x, lv.y);
-                attn::ffma2(o[2], o[3], f, f, lv.z, lv.w);
+              for (int k = 0; k < CW; k += 16) {
+                float4 ks[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ks[e] = decltype(fresh)::value ? lds4(sc + c + k + 4 * e) : *reinterpret_cast<const float4*>(sc + c + k + 4 * e);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  attn::fmul2(v[k + 4 * e], v[k + 4 * e + 1], ks[e].x, ks[e].y);
+                  attn::fmul2(v[k + 4 * e + 2], v[k + 4 * e + 3], ks[e].z, ks[e].w);
+                }
               }
             }
-          }
-          if (masked) {
+            if (masked) {
 #pragma unroll
-            for (int k = 0; k < TN; ++k)
-              if (t * TN + k > lim) v[k] = -INFINITY;
+              for (int k = 0; k < CW; ++k)
+                if (t * TN + c + k > lim) v[k] = -INFINITY;
+            }
+            use(v, c);
           }
         };
-        load_s();
         // After a row's first tile the maximum rarely moves: the factors are taken against the old one, and
         // their sum tells whether that was safe (below 2^15 every one fits fp16).  Otherwise, and on a row's first
         // tile, the tile's maximum is taken first, and O rescaled if it moves.
         float l_tile = 0.0f;
+        float sv_top = 1.0f;
+        if (TOK) {
+          const float4 y = *reinterpret_cast<const float4*>(sc + 3 * TN + 4);
+          sv_top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+        }
+        uint32_t hp[TN / 2];
         bool exact = __any_sync(0xffffffffu, m_run == -INFINITY);
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
           if (exact) {
             float mx[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              mx[e] = v[e];
+            for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
+            scores([&](float(&v)[CW], int c) {
+              if (TOK) {
 #pragma unroll
-              for (int q = 1; q < TN / 8; q += 2)
-                mx[e] = q + 1 < TN / 8 ? attn::fmax3(mx[e], v[e + 8 * q], v[e + 8 * q + 8]) : fmaxf(mx[e], v[e + 8 * q]);
-            }
+                for (int k = 0; k < CW; ++k) v[k] = fmaf(v[k], f, __log2f(sc[TN + c + k]));
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int q = 0; q < CW / 8; q += 2) mx[e] = attn::fmax3(mx[e], v[e + 8 * q], v[e + 8 * q + 8]);
+            }, Bool<true>{});
             const float mt = attn::fmax3(attn::fmax3(mx[0], mx[1], mx[2]), attn::fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
             const float mts = TOK || mt == -INFINITY ? mt : mt * f;
             const float m_new = mts > m_run + 8.0f ? mts : m_run;
@@ -608,49 +640,50 @@ __global__ void __launch_bounds__(CT, 1)
           }
           // scores past 2^20: v f and the rounded maximum would differ by more than an exponent can bear, so
           // the maximum is taken off before f
-          const bool far = !TOK && __any_sync(0xffffffffu, m_run > -INFINITY && fabsf(m_run) > 0x1p20f);
-          const float nb = m_run == -INFINITY ? 0.0f : kShift - (far ? 0.0f : m_run);
-          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (far) {
+          const bool far = __any_sync(0xffffffffu, m_run > -INFINITY && fabsf(m_run) > 0x1p20f);
+          // (per-token modes: after f's own rounding, which the maximum has had too)
+          const float fe = TOK && far ? 1.0f : f;
+          const float nb = m_run == -INFINITY ? 0.0f : kShift - (far && !TOK ? 0.0f : m_run);
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          scores([&](float(&v)[CW], int c) {
+            if (far) {
 #pragma unroll
-            for (int k = 0; k < TN; ++k) v[k] -= m_raw;
-          }
-#pragma unroll
-          for (int k = 0; k < TN; k += 4) {
-            if (TOK) {
-              attn::fadd2(v[k], v[k + 1], nb, nb);
-              attn::fadd2(v[k + 2], v[k + 3], nb, nb);
-            } else {
-              attn::ffma2(v[k], v[k + 1], f, f, nb, nb);
-              attn::ffma2(v[k + 2], v[k + 3], f, f, nb, nb);
+              for (int k = 0; k < CW; ++k) v[k] = TOK ? v[k] * f : v[k] - m_raw;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[k + e] = attn::ex2(v[k + e]);
-            attn::fadd2(ls[0], ls[1], v[k], v[k + 1]);
-            attn::fadd2(ls[2], ls[3], v[k + 2], v[k + 3]);
-            if (TOK) {
-              const float4 iv = lds4(sc + 2 * TN + k);
-              // in place (volatile): the compiler would put these off, and spill the factors meanwhile
-              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[0]) : "f"(v[k]), "f"(iv.x));
-              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[1]) : "f"(v[k + 1]), "f"(iv.y));
-              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[2]) : "f"(v[k + 2]), "f"(iv.z));
-              asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(lp[3]) : "f"(v[k + 3]), "f"(iv.w));
+            for (int k = 0; k < CW; k += 16) {
+              float4 vs[4];
+              if (TOK) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) vs[e] = *reinterpret_cast<const float4*>(sc + TN + c + k + 4 * e);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float* o = &v[k + 4 * e];
+                attn::ffma2(o[0], o[1], fe, fe, nb, nb);
+                attn::ffma2(o[2], o[3], fe, fe, nb, nb);
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) o[i4] = attn::ex2(o[i4]);
+                attn::fadd2(ls[0], ls[1], o[0], o[1]);
+                attn::fadd2(ls[2], ls[3], o[2], o[3]);
+                if (TOK) {
+                  attn::fmul2(o[0], o[1], vs[e].x, vs[e].y);
+                  attn::fmul2(o[2], o[3], vs[e].z, vs[e].w);
+                }
+                const __half2 h0 = __floats2half2_rn(o[0], o[1]), h1 = __floats2half2_rn(o[2], o[3]);
+                hp[(c + k) / 2 + 2 * e] = *reinterpret_cast<const uint32_t*>(&h0);
+                hp[(c + k) / 2 + 2 * e + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+              }
             }
-          }
-          const float w = (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          l_tile = TOK ? (lp[0] + lp[1]) + (lp[2] + lp[3]) : w;
+          }, Bool<false>{});
+          l_tile = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          // the sum (times the tile's largest s_v) is above every factor
+          const float w = TOK ? l_tile * sv_top : l_tile;
           if (exact || !__any_sync(0xffffffffu, !(w < 32768.0f))) break;
           exact = true;
-          load_s();
         }
         if (!ok) break;
         // ---- P: the factors as fp16, over S
-        uint32_t hp[TN / 2];
-#pragma unroll
-        for (int k = 0; k < TN; k += 2) {
-          const __half2 hv = __floats2half2_rn(v[k], v[k + 1]);
-          hp[k / 2] = *reinterpret_cast<const uint32_t*>(&hv);
-        }
         tmem_st32(tS + loff, *reinterpret_cast<uint32_t(*)[32]>(&hp[0]));
         tmem_st32(tS + loff + 32, *reinterpret_cast<uint32_t(*)[32]>(&hp[32]));
         tmem_st_wait();
@@ -784,8 +817,8 @@ cudaError_t launch_paged_chunk(const PagedAttnArgs& a, void* ws, cudaStream_t s)
   plan_carve<CPL<false>>(p, ws, D, grid);
   CUtensorMap mk, mv;
   cudaError_t e;
-  if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, UR, false)) != cudaSuccess) return e;
-  if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, UR, false)) != cudaSuccess) return e;
+  if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, 8192 / D, false)) != cudaSuccess) return e;
+  if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, 8192 / D, false)) != cudaSuccess) return e;
   return D == 128 ? launch_mode<128, false>(mk, mv, p, a.cache->mode, grid, s)
                   : launch_mode<64, true>(mk, mv, p, a.cache->mode, grid, s);
 }

@@ -5,25 +5,19 @@
 // kernel, whose 128-row tiles they fill.  D = 64: all to the chunk kernel.
 #include <cuda_runtime.h>
 
-#include "internal.cuh"
+#include "paged_sched.cuh"
 
 namespace faq {
 
-// Query rows per kv head that a sequence of the batch can have.
-static long long most_rows(const PagedAttnArgs& a) {
-  const int max_q = a.batch->cu_q ? (a.batch->max_q > 0 ? (a.batch->max_q < a.q->T ? a.batch->max_q : a.q->T) : a.q->T) : 1;
-  return (long long)max_q * (a.q->H / a.cache->H);
-}
-
 size_t paged_attention_ws(const PagedAttnArgs& a) {
   const int D = a.q->D;
-  if (D == 128 && most_rows(a) <= 16) return paged_decode_ws();
+  if (D == 128 && paged_most_rows(a) <= 16) return paged_decode_ws();
   return paged_chunk_ws(D);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   const int D = a.q->D;
-  const long long rows = most_rows(a);
+  const long long rows = paged_most_rows(a);
   if (D == 128) {
     // sequences of up to 16 query rows per kv head, then those of more
     const cudaError_t e = launch_paged_decode(a, rows < 16 ? (int)rows : 16, ws, s);

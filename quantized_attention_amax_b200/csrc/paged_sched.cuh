@@ -273,6 +273,12 @@ inline paged::AttnP paged_attn_params(const PagedAttnArgs& a) {
   return p;
 }
 
+// Query rows per kv head that a sequence of the batch can have.
+inline long long paged_most_rows(const PagedAttnArgs& a) {
+  const int T = a.q->T, max_q = a.batch->max_q > 0 && a.batch->max_q < T ? a.batch->max_q : T;
+  return (long long)(a.batch->cu_q ? max_q : 1) * (a.q->H / a.cache->H);
+}
+
 // Tensor map over a cache's codes: boxes of one page's (at most `keys`) rows of one head, with the swizzle of
 // MMA operands of that row length (128 or 64 bytes) or rows one behind the other.  A page index past the pool
 // reads zeros.

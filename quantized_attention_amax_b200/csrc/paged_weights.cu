@@ -2,241 +2,404 @@
 // softmax matrix):  w_j = sum over the rows r of a kv head that see j of 2^(x_rj - log2(e) lse_r),
 // x_rj = log2(e) softmax_scale s_k(j) q_r . k_j.
 //
-// With one new token per sequence the K codes' bytes bound it; with a window of tokens the products and
-// exponentials do.  The keys are the MMA's 16 rows (they stay in registers, as fp16) and the query rows its
-// columns, 8 at a time, from shared memory: a key's weight is then summed along the columns a thread
-// holds and over its quad, in a fixed order, and no two threads write one key.  A warp takes 16 keys,
-// a unit is 128 keys of one (sequence, kv head), and the CTAs take equal runs of units counted from the lengths
-// on the device.
-#include <cuda_bf16.h>
-
-#include "paged_common.cuh"
+// With one new token per sequence the K codes' bytes bound it; with a window of tokens the exponentials and what
+// surrounds them do.  As in the decode kernel the codes are MMA operands as TMA leaves them and the query
+// rows enter as three 8-bit digits each (paged_digits.cuh):  S^T [128 keys x 3 rows] = K . Q^T.  A thread owns a
+// key: it joins the digits' sums, takes the exponential and adds up along its rows, so a key's weight is summed in a
+// fixed order by one thread, and no two threads write one key.  Up to 256 rows stay in shared memory; a
+// sequence with more is walked once per 256 rows, adding to what the walk before left.  Two warpgroups take the key
+// tiles in turn (64 rows of one tile at a time each), so one's MMAs run under the other's exponentials.
+// Units are 128 keys of one (sequence, kv head); the CTAs take equal runs of them, counted from the lengths on
+// the device.
+#include "paged_digits.cuh"
+#include "paged_sched.cuh"
 
 namespace faq {
 namespace {
 using namespace paged;
 
-constexpr int WW = 8;        // warps per CTA
-constexpr int WUK = WW * 16; // keys per unit
-constexpr int WR = 64;       // query rows in shared memory at a time
+constexpr int TK = 128;      // keys per tile
+constexpr int NKS = 4;       // K tiles in flight
+constexpr int QR = 256;      // query rows in shared memory
+constexpr int WT = 384;      // warp 0 loads, warp 1 MMAs, warps 4-7 and 8-11 the weights
 
 struct WeightP {
-  const __nv_bfloat16* q;
-  long long q_stride;
-  Cache c;
-  Batch bt;
-  int Hq, G, causal, accumulate;
-  float scale_log2;
-  const float* lse;
+  AttnP a;
+  int accumulate;
   float* acc;
   long long acc_stride;
-  int* status;
 };
 
-// A row's constants: x - lse2 is sum * f * s_k - hi - lo; lim: the last key it sees (-1: none).
+// A row's constants: x - lse2 is sum * s_k * f - hi - lo; lim: the last key it sees.
 struct __align__(16) RowC {
   float f, hi, lo;
   int lim;
 };
 
-template <int D>
-struct WS {
-  static constexpr uint32_t QROW = 2 * D + 16;  // bytes per fp16 row; the pad spreads rows over the banks
-  static constexpr uint32_t ROWC = WR * QROW;
-  static constexpr uint32_t TOTAL = ROWC + WR * 16;
+// R rows to a group of 3 R columns: digit k of row r of the group is column k R + r.  Groups of 16 rows come in
+// steps of up to four (N = 48 .. 192 columns); up to 4 rows in all take one group of 4 (N = 16).
+template <int D, int R>
+struct WL {
+  static constexpr int GC = R == 4 ? 16 : 48;          // columns of a group
+  static constexpr int GS = R == 4 ? 1 : 4;            // groups of a step
+  static constexpr int ROWS = R == 4 ? 4 : QR;
+  static constexpr uint32_t TILE = TK * D;
+  static constexpr uint32_t Q = 0;                     // [ROWS / R groups][GC][D] digits, swizzled
+  static constexpr uint32_t K = (ROWS / R * GC * D + 1023) & ~1023u;
+  static constexpr uint32_t ROW = K + NKS * TILE;
+  static constexpr uint32_t BAR = ROW + ROWS * 16;
+  static constexpr uint32_t TOTAL = BAR + 256;
+  static constexpr uint32_t ALLOC = TOTAL + 1024;
 };
 
+enum { W_KF = 0, W_KE = W_KF + NKS, W_Q = W_KE + NKS, W_QD, W_SF, W_SE = W_SF + 2, W_FIN = W_SE + 2, W_COUNT };
+
 __device__ __forceinline__ int weight_units(const WeightP& p, int b, Seq& s) {
-  s = load_seq(p.bt, p.c.page_shift, b, p.status, 221);
+  s = load_seq(p.a.bt, p.a.c.page_shift, b, p.a.status, 221);
   if (s.n > p.acc_stride) {
-    bad(p.status, 222);
+    bad(p.a.status, 222);
     s = {0, 0, 0};
   }
-  return s.m > 0 || !p.accumulate ? (s.n + WUK - 1) / WUK : 0;
+  return s.m > 0 || !p.accumulate ? (s.n + TK - 1) / TK : 0;
 }
 
-template <int D, bool FP8, bool TOK>
-__global__ void __launch_bounds__(WW * 32) paged_weights_kernel(const WeightP p) {
-  using L = WS<D>;
-  constexpr int KC = D / 64;
-  __shared__ __align__(16) uint8_t smem[L::TOTAL];
-  RowC* rowc = reinterpret_cast<RowC*>(smem + L::ROWC);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
+// The CTA's run, piece by piece: key tiles [t0, t1) of one (sequence, kv head).
+struct WRun {
+  int b, hk, nt, t0, t1;
+  Seq s;
+  long long left;  // units of the run from t0 on
+  __device__ __forceinline__ void piece() { t1 = (int)(left < nt - t0 ? t0 + left : nt); }
+  __device__ __forceinline__ bool next(const WeightP& p) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++hk == p.a.c.H) {
+      hk = 0;
+      do {
+        if (++b >= p.a.bt.B) return false;  // cannot be while the lengths stay as they were counted
+        nt = weight_units(p, b, s);
+      } while (nt == 0);
+    }
+    piece();
+    return true;
+  }
+};
 
+template <int D, bool FP8, bool TOK, int R>
+__global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_constant__ CUtensorMap tmk, const WeightP wp) {
+  using L = WL<D, R>;
+  constexpr uint32_t SW = D == 128 ? kSwz128 : kSwz64, SBO = 8 * D;
+  const AttnP& p = wp.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + W_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- the run: units [total c / grid, total (c + 1) / grid)
   long long total = 0;
   for (int b = lane; b < p.bt.B; b += 32) {
     Seq s;
-    total += weight_units(p, b, s);
+    total += weight_units(wp, b, s);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   total *= p.c.H;
   const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
   if (u0 >= u1) return;
-  // the sequence of unit u0
-  int b = -1;
-  Seq s = {0, 0, 0};
-  int nt = 0;
-  long long first = 0;
+  WRun run = {};
+  run.b = -1;
   {
     long long base = 0;
-    for (int b0 = 0; b0 < p.bt.B && b < 0; b0 += 32) {
+    for (int b0 = 0; b0 < p.bt.B && run.b < 0; b0 += 32) {
       Seq x = {0, 0, 0};
-      const int n = b0 + lane < p.bt.B ? weight_units(p, b0 + lane, x) : 0;
-      const long long mine = (long long)n * p.c.H;
-      long long end = mine;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, end, off);
-        if (lane >= off) end += o;
-      }
-      const unsigned after = __ballot_sync(0xffffffffu, base + end > u0);
+      const int n = b0 + lane < p.bt.B ? weight_units(wp, b0 + lane, x) : 0;
+      const long long mine = (long long)n * p.c.H, end = base + lanes_before(mine, lane);
+      const unsigned after = __ballot_sync(0xffffffffu, end > u0);
       if (after) {
         const int src = __ffs(after) - 1;
-        b = b0 + src;
-        s.q0 = __shfl_sync(0xffffffffu, x.q0, src);
-        s.m = __shfl_sync(0xffffffffu, x.m, src);
-        s.n = __shfl_sync(0xffffffffu, x.n, src);
-        nt = __shfl_sync(0xffffffffu, n, src);
-        first = base + __shfl_sync(0xffffffffu, end - mine, src);
+        run.b = b0 + src;
+        run.s.q0 = __shfl_sync(0xffffffffu, x.q0, src);
+        run.s.m = __shfl_sync(0xffffffffu, x.m, src);
+        run.s.n = __shfl_sync(0xffffffffu, x.n, src);
+        run.nt = __shfl_sync(0xffffffffu, n, src);
+        const long long at = u0 - __shfl_sync(0xffffffffu, end - mine, src);
+        run.hk = (int)(at / run.nt);
+        run.t0 = (int)(at - (long long)run.hk * run.nt);
       }
-      base += __shfl_sync(0xffffffffu, end, 31);
+      base = __shfl_sync(0xffffffffu, end, 31);
     }
   }
-  int hk = (int)((u0 - first) / nt), tile = (int)((u0 - first) % nt);
-  int held = -1;  // the (row block of the) item whose Q rows are in shared memory
+  run.left = u1 - u0;
+  run.piece();
 
-  for (long long u = u0; u < u1; ++u) {
-    const int rows = s.m * p.G;
-    const int nblk = (rows + WR - 1) / WR;
-    // ---- this warp's 16 keys: rows g and g + 8 of the A fragments
-    const int k0 = tile * WUK + warp * 16;
-    uint32_t ka[D / 16][4];
-    float ksc[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int j = k0 + g + 8 * x;
-      const int pg = j < s.n ? page_of(p.bt, p.c, b, j, p.status, 223) : -1;
-      const uint8_t* src = p.c.k + (pg >= 0 ? p.c.row(pg, hk, j & p.c.page_mask) : 0);
-      ksc[x] = TOK ? (pg >= 0 ? __ldg(p.c.ks + p.c.scale(pg, hk, j & p.c.page_mask)) : 0.0f) : __ldg(p.c.ks + hk);
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint4 kw = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(src) + t + 4 * c) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) codes4_to_h2<FP8>(w[k], ka[4 * c + k][x], ka[4 * c + k][2 + x]);
-      }
+  if (tid == 0) {
+    for (int i = 0; i < NKS; ++i) {
+      mbar_init(&bar[W_KF + i], 1);
+      mbar_init(&bar[W_KE + i], 1);
     }
-    float sum[2] = {0.0f, 0.0f};
-    for (int blk = 0; blk < nblk; ++blk) {
-      // ---- Q rows of the block as fp16, and their constants
-      if (held != blk || nblk > 1) {
-        __syncthreads();
-        for (int r = warp; r < (min(rows - blk * WR, WR) + 7) / 8 * 8; r += WW) {
-          const int rr = blk * WR + r;
-          const int i = rr / p.G;
-          const bool ok = rr < rows;
-          const long long row = (long long)(s.q0 + i);
-          const int hq = hk * p.G + rr - i * p.G;
-          uint32_t w[D / 64];  // D / 32 elements per lane
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + row * p.q_stride + (long long)hq * D);
+    mbar_init(&bar[W_Q], 256);
+    mbar_init(&bar[W_QD], 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar[W_SF + i], 1);
+      mbar_init(&bar[W_SE + i], 4);
+    }
+    mbar_init(&bar[W_FIN], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  auto walks = [&]() { return (run.s.m * p.G + L::ROWS - 1) / L::ROWS; };  // of the piece's tiles
+  auto wait = [&](int which, int phase, int where) { return mbar_wait(&bar[which], phase & 1, abort_flag, p.status, where); };
+  auto wwait = [&](int which, int phase, int where) { return __all_sync(0xffffffffu, wait(which, phase, where)); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loads
+    const int box = min(TK, p.c.page_mask + 1), nbox = TK / box;
+    if (lane == 0) tma_prefetch_desc(&tmk);
+    int j = 0;
+    bool ok = true;
+    do {
+      const int b = run.b, hk = run.hk, n = run.s.n;
+      auto page = [&](int t) {
+        const int k0 = t * TK + lane * box;
+        int pg = p.c.pages;  // past the end, or not a page of the cache: one past the pool, read as zeros
+        if (t < run.t1 && lane < nbox && k0 < n) {
+          pg = page_of(p.bt, p.c, b, k0, p.status, 223);
+          if (pg < 0) pg = p.c.pages;
+        }
+        return pg;
+      };
+      const int nw = walks();
+      for (int w = 0; w < nw && ok; ++w) {
+        int pg = page(run.t0);
+        for (int t = run.t0; t < run.t1 && ok; ++t, ++j) {
+          const int next = page(t + 1), s = j % NKS;
+          const int off = (t * TK + lane * box) & p.c.page_mask;
+          if (j >= NKS && !(ok = wwait(W_KE + s, j / NKS - 1, 261))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar[W_KF + s], L::TILE);
+          __syncwarp();
+          if (lane < nbox)
+            tma_load_4d(smem + L::K + s * L::TILE + lane * box * D, &tmk, &bar[W_KF + s], 0, p.c.bnsd ? off : hk,
+                        p.c.bnsd ? hk : off, pg);
+          pg = next;
+        }
+      }
+    } while (ok && run.next(wp));
+    if (*abort_flag)
+      for (int t = max(0, j - NKS); t < j; ++t) mbar_drain(&bar[W_KF + t % NKS], (t / NKS) & 1);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      const uint32_t sQ = smem_u32(smem + L::Q), sK = smem_u32(smem + L::K);
+      int j = 0, nq = 0, steps[2] = {0, 0};
+      bool ok = true;
+      do {
+        const int rows = run.s.m * p.G, nw = walks();
+        for (int w = 0; w < nw && ok; ++w, ++nq) {
+          if (!(ok = wait(W_Q, nq, 262))) break;
+          tc_fence_after();
+          const int groups = (min(rows - w * L::ROWS, L::ROWS) + R - 1) / R;
+          // two tiles at a time, one to a warpgroup, their steps in turn
+          for (int t = run.t0; t < run.t1 && ok; t += 2, j += 2) {
+            const int n = min(2, run.t1 - t);
+            for (int g = 0; g < groups && ok; g += L::GS) {
+              const int gn = min(L::GS, groups - g);
+              const uint32_t idesc = FP8 ? make_idesc(kAccF32, kFmtE4M3, kFmtE4M3, 0, 0, gn * L::GC, 128)
+                                         : make_idesc(kAccS32, kFmtS8, kFmtS8, 0, 0, gn * L::GC, 128);
+              for (int x = 0; x < n && ok; ++x) {
+                const int s = (j + x) % NKS;
+                if (g == 0) ok = wait(W_KF + s, (j + x) / NKS, 263);
+                if (ok && steps[x] > 0) ok = wait(W_SE + x, steps[x] - 1, 264);
+                if (!ok) break;
+                ++steps[x];
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk) {
+                  const uint64_t da = make_sdesc(sK + s * L::TILE + kk * 32, 16, SBO, SW);
+                  const uint64_t db = make_sdesc(sQ + g * L::GC * D + kk * 32, 16, SBO, SW);
+                  if (FP8)
+                    mma_f8f6f4(tbase + x * 256, da, db, idesc, kk > 0);
+                  else
+                    mma_i8(tbase + x * 256, da, db, idesc, kk > 0);
+                }
+                mma_commit(&bar[W_SF + x]);
+                if (g + L::GS >= groups) mma_commit(&bar[W_KE + s]);
+              }
+            }
+            if (n == 1) --j;  // an odd last tile
+          }
+        }
+      } while (ok && run.next(wp));
+      mma_commit(&bar[W_FIN]);
+      mbar_drain(&bar[W_FIN], 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- weights
+    const int x = (warp - 4) >> 2;             // warpgroup: the tiles of its turn
+    const int wt = tid - 128;                  // of the 256 threads
+    const int i = (warp & 3) * 32 + lane;      // key of the tile, TMEM lane
+    const uint32_t loff = (uint32_t)((warp & 3) * 32) << 16;
+    RowC* rowc = reinterpret_cast<RowC*>(smem + L::ROW);
+    int nq = 0, steps = 0;
+    bool ok = true;
+    do {
+      const Seq s = run.s;
+      const int hk = run.hk, b = run.b, rows = s.m * p.G, nw = walks();
+      float* acc = wp.acc + ((long long)b * p.c.H + hk) * wp.acc_stride;
+      if (nw == 0)  // no new token, not accumulating: zeros
+        for (int j = run.t0 * TK + wt; j < min(run.t1 * TK, s.n); j += 256) acc[j] = 0.0f;
+      for (int w = 0; w < nw && ok; ++w, ++nq) {
+        // ---- Q digits and the rows' constants, D / 16 lanes a row, once the MMAs of the walk before are done
+        if (nq > 0) {
+          mbar_arrive(&bar[W_QD]);
+          if (!(ok = wwait(W_QD, nq - 1, 265))) break;
+        }
+        constexpr int LPR = D / 16;
+        const int here = min(rows - w * L::ROWS, L::ROWS), groups = (here + R - 1) / R;
+        for (int idx = wt; idx - lane < groups * R * LPR; idx += 256) {
+          const int rl = idx / LPR, c = idx % LPR, r = w * L::ROWS + rl, ii = r / p.G;
+          const bool in = idx < groups * R * LPR, live = in && r < rows;
+          const int hq = hk * p.G + r - ii * p.G;
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride + (long long)hq * D + c * 16);
+          uint4 raw[2];
+          raw[0] = live ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          raw[1] = live ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+          const uint32_t* wv = &raw[0].x;
           float m = 0.0f;
+          bool bad_value = false;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            w[c] = ok ? __ldg(src + lane * (D / 64) + c) : 0u;
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[c] << 16)), fabsf(__uint_as_float(w[c] & 0xFFFF0000u))));
+          for (int e = 0; e < 8; ++e) {
+            const float y0 = fabsf(__uint_as_float(wv[e] << 16)), y1 = fabsf(__uint_as_float(wv[e] & 0xFFFF0000u));
+            bad_value = bad_value || y0 != y0 || y1 != y1;
+            m = fmaxf(m, fmaxf(y0, y1));
           }
+          if (bad_value) m = INFINITY;
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          for (int off = LPR / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
           float inv;
-          const float sc = pow2_to_fp16(m, inv);
+          const float sc = digit_scale<FP8>(m, inv);
+          uint32_t dw[3][4] = {};
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(w[c] << 16) * sc, __uint_as_float(w[c] & 0xFFFF0000u) * sc);
-            *reinterpret_cast<__half2*>(smem + r * L::QROW + (lane * (D / 64) + c) * 4) = h;
+          for (int e = 0; e < 16; ++e) {
+            uint32_t d[3];
+            const float y = __uint_as_float((e & 1) ? wv[e >> 1] & 0xFFFF0000u : wv[e >> 1] << 16);
+            q_digits<FP8>(sc == 0.0f ? 0.0f : y, sc, d);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) dw[k][e >> 2] |= d[k] << (8 * (e & 3));
           }
-          if (lane == 0) {
-            const float lse = ok ? __ldg(p.lse + row * p.Hq + hq) : -INFINITY;
+          if (!in) continue;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t col = rl / R * L::GC + k * R + rl % R;
+            *reinterpret_cast<uint4*>(smem + L::Q + (D == 128 ? swz128_offset(col, c) : swz64_offset(col, c))) =
+                make_uint4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
+          }
+          if (c == 0) {
+            const float lse = live ? __ldg(p.lse + (long long)(s.q0 + ii) * p.Hq + hq) : -INFINITY;
             RowC rc;
             rc.f = p.scale_log2 * inv;
-            rc.lim = !ok || lse == -INFINITY ? -1 : p.causal ? min(s.n - 1, s.n - s.m + i) : s.n - 1;
-            // log2(e) lse in two terms: log2(e) = 1.4427... as fp32 plus its remainder
-            rc.hi = rc.lim < 0 ? 0.0f : lse * 1.44269502f;
+            rc.lim = lse == -INFINITY ? -1 : row_limit(p, s, r);
+            // log2(e) lse in two terms: log2(e) is 1.442695... as fp32 plus its remainder; rows that give
+            // nothing: so far down that every exponential is 0
+            rc.hi = rc.lim < 0 ? 1e30f : lse * 1.44269502f;
             rc.lo = rc.lim < 0 ? 0.0f : fmaf(lse, 1.44269502f, -rc.hi) + lse * 1.92596303e-8f;
-            rowc[r] = rc;
+            rowc[rl] = rc;
           }
         }
-        __syncthreads();
-        held = blk;
-      }
-      const int nn = (min(rows - blk * WR, WR) + 7) / 8;
-      for (int n = 0; n < nn; ++n) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const uint8_t* qrow = smem + (n * 8 + g) * L::QROW;
+        fence_async_smem();
+        mbar_arrive(&bar[W_Q]);
+        if (!(ok = wwait(W_Q, nq, 266))) break;
+        const int lim_lo = p.causal ? s.n - s.m + w * L::ROWS / p.G : s.n - 1;  // every row of the walk sees the keys up to here
+        // ---- this warpgroup's tiles
+        float sk_next = 0.0f;
+        auto load_scale = [&](int t) {
+          const int key = t * TK + i;
+          if (!TOK) return __ldg(p.c.ks + hk);
+          if (t >= run.t1 || key >= s.n) return 0.0f;
+          const int pg = page_of(p.bt, p.c, b, key, p.status, 223);
+          return pg >= 0 ? __ldg(p.c.ks + p.c.scale(pg, hk, key & p.c.page_mask)) : 0.0f;
+        };
+        if (run.t0 + x < run.t1) sk_next = load_scale(run.t0 + x);
+        for (int t = run.t0 + x; t < run.t1 && ok; t += 2) {
+          const int key = t * TK + i;
+          const float sk = sk_next;
+          sk_next = TOK ? load_scale(t + 2) : sk;
+          const bool add = wp.accumulate || w > 0;
+          const float old = add && key < s.n ? acc[key] : 0.0f;
+          const bool masked = t * TK + TK - 1 > lim_lo;
+          float sum[2] = {0.0f, 0.0f};
+          for (int g = 0; g < groups && ok; g += L::GS, ++steps) {
+            if (!(ok = wwait(W_SF + x, steps, 267))) break;
+            tc_fence_after();
+            const int gn = min(L::GS, groups - g);
+#pragma unroll 1
+            for (int q = 0; q < gn; ++q) {
+              uint32_t a[L::GC];
 #pragma unroll
-        for (int c = 0; c < KC; ++c)
+              for (int c = 0; c < L::GC / 16; ++c)
+                tmem_ld16(tbase + x * 256 + q * L::GC + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
+              tmem_ld_wait();
+              const RowC* rq = rowc + (g + q) * R;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {  // MMA steps 4 c + 2 y and + 1: dims 16 (t + 4 c) + 8 y .. + 7
-            const uint4 qv = *reinterpret_cast<const uint4*>(qrow + (t + 4 * c) * 32 + y * 16);
-            mma16816(d, ka[4 * c + 2 * y], qv.x, qv.y);
-            mma16816(d, ka[4 * c + 2 * y + 1], qv.z, qv.w);
+              for (int r = 0; r < R; ++r) {
+                const RowC rc = rq[r];
+                const float y = join_digits<FP8>(a[r], a[R + r], a[2 * R + r]) * sk;
+                float e = attn::ex2(fmaf(y, rc.f, -rc.hi) - rc.lo);
+                if (masked) e = key <= rc.lim ? e : 0.0f;
+                sum[r & 1] += e;
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[W_SE + x]);
           }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const RowC rc = rowc[n * 8 + 2 * t + e];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int j = k0 + g + 8 * x;
-            const float v = attn::ex2(fmaf(d[2 * x + e] * ksc[x], rc.f, -rc.hi) - rc.lo);
-            sum[x] += j <= rc.lim ? v : 0.0f;
-          }
+          if (ok && key < s.n) acc[key] = old + (sum[0] + sum[1]);
         }
       }
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-    }
-    if (t < 2) {
-      const int j = k0 + g + 8 * t;
-      if (j < s.n) {
-        float* dst = p.acc + ((long long)b * p.c.H + hk) * p.acc_stride + j;
-        const float w = t ? sum[1] : sum[0];
-        *dst = p.accumulate ? *dst + w : w;
-      }
-    }
-    // ---- the next unit
-    if (++tile == nt) {
-      tile = 0;
-      held = -1;
-      if (++hk == p.c.H) {
-        hk = 0;
-        if (u + 1 < u1) {
-          do {
-            if (++b >= p.bt.B) return;  // cannot be while the lengths stay as they were counted
-            nt = weight_units(p, b, s);
-          } while (nt == 0);
-        }
-      }
-    }
+    } while (ok && run.next(wp));
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
   }
 }
 
-template <int D, bool FP8, bool TOK>
-cudaError_t launch_d(const WeightP& p, cudaStream_t s) {
-  paged_weights_kernel<D, FP8, TOK><<<2 * sm_count(), WW * 32, 0, s>>>(p);
+template <int D, bool FP8, bool TOK, int R>
+cudaError_t launch_r(const CUtensorMap& mk, const WeightP& p, cudaStream_t s) {
+  using L = WL<D, R>;
+  static_assert(L::ALLOC <= 227 * 1024, "shared memory per CTA");
+  auto kern = paged_weights_kernel<D, FP8, TOK, R>;
+  cudaError_t e;
+  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), L::ALLOC)) != cudaSuccess) return e;
+  kern<<<sm_count(), WT, L::ALLOC, s>>>(mk, p);
   return cudaGetLastError();
 }
 
+template <int D, bool FP8, bool TOK>
+cudaError_t launch_d(const CUtensorMap& mk, const WeightP& p, long long rows, cudaStream_t s) {
+  return rows <= 4 ? launch_r<D, FP8, TOK, 4>(mk, p, s) : launch_r<D, FP8, TOK, 16>(mk, p, s);
+}
+
 template <int D>
-cudaError_t launch_mode(const WeightP& p, int mode, cudaStream_t s) {
+cudaError_t launch_mode(const CUtensorMap& mk, const WeightP& p, int mode, long long rows, cudaStream_t s) {
   switch (mode) {
-    case FA_MODE_INT8_PER_HEAD: return launch_d<D, false, false>(p, s);
-    case FA_MODE_FP8_PER_HEAD: return launch_d<D, true, false>(p, s);
-    case FA_MODE_INT8_PER_TOKEN: return launch_d<D, false, true>(p, s);
-    case FA_MODE_FP8_PER_TOKEN: return launch_d<D, true, true>(p, s);
+    case FA_MODE_INT8_PER_HEAD: return launch_d<D, false, false>(mk, p, rows, s);
+    case FA_MODE_FP8_PER_HEAD: return launch_d<D, true, false>(mk, p, rows, s);
+    case FA_MODE_INT8_PER_TOKEN: return launch_d<D, false, true>(mk, p, rows, s);
+    case FA_MODE_FP8_PER_TOKEN: return launch_d<D, true, true>(mk, p, rows, s);
     default: return cudaErrorNotSupported;
   }
 }
@@ -245,20 +408,15 @@ cudaError_t launch_mode(const WeightP& p, int mode, cudaStream_t s) {
 
 cudaError_t launch_paged_weights(const PagedAttnArgs& a, cudaStream_t s) {
   WeightP p = {};
-  p.q = static_cast<const __nv_bfloat16*>(a.q->data);
-  p.q_stride = a.q->stride;
-  p.c = paged_cache_of(*a.cache);
-  p.bt = paged_batch_of(*a.batch, a.q->T);
-  p.Hq = a.q->H;
-  p.G = a.q->H / a.cache->H;
-  p.causal = a.causal;
+  p.a = paged_attn_params(a);
   p.accumulate = a.accumulate;
-  p.scale_log2 = (a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf((float)a.q->D)) * 1.4426950408889634f;
-  p.lse = a.lse;
   p.acc = a.acc;
   p.acc_stride = a.acc_stride;
-  p.status = a.status;
-  return a.q->D == 128 ? launch_mode<128>(p, a.cache->mode, s) : launch_mode<64>(p, a.cache->mode, s);
+  CUtensorMap mk;
+  const cudaError_t e = make_page_map(&mk, a.cache->k_codes, *a.cache, TK, true);
+  if (e != cudaSuccess) return e;
+  const long long rows = paged_most_rows(a);
+  return a.q->D == 128 ? launch_mode<128>(mk, p, a.cache->mode, rows, s) : launch_mode<64>(mk, p, a.cache->mode, rows, s);
 }
 
 }  // namespace faq

@@ -8,7 +8,7 @@
 //   2. the kept indices in order: each warp counts its part's scores above the threshold and equal to
 //      it, the counts before it give its places, and of the equal ones the lowest indices are taken;
 //   3. the rows, in rounds: every CTA of the cluster brings its share of the round's kept rows into
-//      shared memory, a cluster barrier, then all are written.  A row's new index is never above its
+//      registers (8 chunks a thread, all on their way at once), a cluster barrier, then all are written.  A row's new index is never above its
 //      old one, so what a round writes lies below every row that later rounds read: the barrier between a
 //      round's reads and its writes is all the order that moving in place needs.
 // The scores (once) and the kept rows (read and written once) bound it; slices are kept in shared
@@ -24,10 +24,11 @@ namespace faq {
 namespace {
 using namespace paged;
 
-constexpr int ET = 512;             // threads per CTA
+constexpr int ET = 1024;            // threads per CTA
 constexpr int EW = ET / 32;
 constexpr int BINS = 2048;
-constexpr int STAGE_BYTES = 144 * 1024;  // keys of the slice, then staged rows
+constexpr int KEY_BYTES = 144 * 1024;  // score bits of the slice
+constexpr int RU = 8;               // rows a thread holds in a round
 
 struct EvictP {
   Cache c;
@@ -48,7 +49,7 @@ __device__ __forceinline__ uint32_t score_bits(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-struct EvictSmem {
+struct __align__(16) EvictSmem {
   uint32_t hist[2][BINS];
   uint32_t warp_sum[EW];
   uint32_t warp_gt[EW], warp_eq[EW];
@@ -58,7 +59,7 @@ struct EvictSmem {
 
 template <int D>
 __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
-  extern __shared__ __align__(16) uint8_t stage[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ EvictSmem sm;
   cg::cluster_group cl = cg::this_cluster();
   const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -93,10 +94,21 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
   const int chunk = (cand + cs - 1) / cs;
   const int lo = min(cand, rank * chunk), cnt = min(cand, lo + chunk) - lo;
   const float* mine = sc + p.sink + lo;
-  uint32_t* keys = reinterpret_cast<uint32_t*>(stage);
-  constexpr int CAP = STAGE_BYTES / 4;
+  constexpr int CAP = KEY_BYTES / 4;
   const int cached = min(cnt, CAP);
-  for (int i = tid; i < cached; i += ET) keys[i] = score_bits(__ldg(mine + i));
+  for (int i0 = 0; i0 < cached; i0 += 8 * ET) {  // eight loads on their way at once
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int i = i0 + q * ET + tid;
+      x[q] = i < cached ? __ldg(mine + i) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int i = i0 + q * ET + tid;
+      if (i < cached) keys[i] = score_bits(x[q]);
+    }
+  }
   auto key = [&](int i) { return i < CAP ? keys[i] : score_bits(__ldg(mine + i)); };
 
   uint32_t thr = 0;
@@ -109,23 +121,23 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
       for (int i = tid; i < BINS; i += ET) hist[i] = 0;
       __syncthreads();
       const uint32_t hi_mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+#pragma unroll 4
       for (int i = tid; i < cnt; i += ET) {
         const uint32_t k = key(i);
         if ((k & hi_mask) == thr) atomicAdd(&hist[(k >> shift) & mask], 1u);
       }
       cl.sync();
-      // this thread's four bins, highest first, summed over the cluster
-      uint32_t mybin[4], sum = 0;
-      const int top = BINS - 1 - 4 * tid;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) mybin[q] = 0;
+      // this thread's two bins, the higher first, summed over the cluster
+      static_assert(BINS == 2 * ET, "two bins a thread");
+      uint32_t mybin[2] = {0, 0};
+      const int top = BINS - 1 - 2 * tid;
+#pragma unroll 8
       for (int r = 0; r < cs; ++r) {
-        const uint32_t* rh = cl.map_shared_rank(hist, r);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mybin[q] += rh[top - q];
+        const uint2 h = *reinterpret_cast<const uint2*>(cl.map_shared_rank(hist, r) + top - 1);
+        mybin[0] += h.y;
+        mybin[1] += h.x;
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) sum += mybin[q];
+      const uint32_t sum = mybin[0] + mybin[1];
       uint32_t incl = sum;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -204,57 +216,61 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
   for (int i = gt0; i < p.recent; i += gts) kept[p.budget - p.recent + i] = n - p.recent + i;
   cl.sync();  // the list is written; the slices' keys are read
 
-  // ---- 3. the rows
-  constexpr int CH = D / 16;                         // 16-byte chunks per code row
-  constexpr int ROW = 2 * D + 8;                     // K, V codes; then the scales
-  constexpr int R = STAGE_BYTES / ROW / 32 * 32;     // rows per CTA and round
-  uint4* srow = reinterpret_cast<uint4*>(stage);     // [R][2 CH]
-  float2* sscale = reinterpret_cast<float2*>(stage + R * 2 * D);
-  for (int base = 0; base < keep; base += cs * R) {
-    const int d0 = base + rank * R, rows = max(0, min(keep - d0, R));
-    // 2 CH lanes a row: the K chunks, then the V chunks
-    const int c = tid % (2 * CH), r0 = tid / (2 * CH);
-    constexpr int RS = ET / (2 * CH);
-    const uint8_t* codes = c < CH ? p.c.k : p.c.v;
-    const int cc = c % CH;
+  if (so)  // the kept tokens' scores
 #pragma unroll 4
-    for (int r = r0; r < rows; r += RS) {
-      const int f = __ldcg(kept + d0 + r);
-      if (f == d0 + r) continue;
-      const int pg = page_of(p.bt, p.c, b, f, p.status, 232);
-      if (pg < 0) continue;
-      srow[r * 2 * CH + c] = __ldcg(reinterpret_cast<const uint4*>(codes + p.c.row(pg, h, f & p.c.page_mask)) + cc);
+    for (int i = gt0; i < keep; i += gts) so[i] = __ldg(sc + __ldcg(kept + i));
+
+  // ---- 3. the rows
+  constexpr int CH = D / 16;               // 16-byte chunks per code row
+  constexpr int RS = ET / (2 * CH);        // rows side by side: 2 CH threads a row, K's chunks, then V's
+  constexpr int R = RU * RS;               // rows per CTA and round
+  const int c = tid % (2 * CH), r0 = tid / (2 * CH), cc = c % CH;
+  uint8_t* codes = c < CH ? p.c.k : p.c.v;
+  float* scales = p.c.per_token ? (c < CH ? p.c.ks : p.c.vs) : nullptr;  // moved by the first of K's and of V's threads
+  const int* table = p.bt.table + (long long)b * p.bt.max_pages;
+  for (int base = 0; base < keep; base += cs * R) {
+    const int d0 = base + rank * R + r0;
+    int f[RU];
+    uint4 row[RU];
+    float scale[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const int d = d0 + u * RS;
+      f[u] = d < keep ? __ldcg(kept + d) : -1;
+      if (f[u] == d) f[u] = -1;  // stays where it is
     }
-    for (int r = tid; r < rows; r += ET) {
-      const int f = __ldcg(kept + d0 + r);
-      if (so) so[d0 + r] = __ldg(sc + f);
-      if (!p.c.per_token || f == d0 + r) continue;
-      const int pg = page_of(p.bt, p.c, b, f, p.status, 232);
-      if (pg < 0) continue;
-      const long long si = p.c.scale(pg, h, f & p.c.page_mask);
-      sscale[r] = make_float2(__ldcg(p.c.ks + si), __ldcg(p.c.vs + si));
+    int pg[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) pg[u] = f[u] >= 0 ? __ldg(table + (f[u] >> p.c.page_shift)) : -1;
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      if (f[u] >= 0 && (unsigned)pg[u] >= (unsigned)p.c.pages) {
+        bad(p.status, 232);
+        f[u] = -1;
+      }
+      if (f[u] >= 0) {
+        const int slot = f[u] & p.c.page_mask;
+        row[u] = __ldcg(reinterpret_cast<const uint4*>(codes + p.c.row(pg[u], h, slot)) + cc);
+        if (scales && cc == 0) scale[u] = __ldcg(scales + p.c.scale(pg[u], h, slot));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const int d = d0 + u * RS;
+      pg[u] = f[u] >= 0 ? __ldg(table + (d >> p.c.page_shift)) : -1;
     }
     cl.sync();  // every row of the round is read
-    uint8_t* dst = c < CH ? p.c.k : p.c.v;
-#pragma unroll 4
-    for (int r = r0; r < rows; r += RS) {
-      const int d = d0 + r, f = __ldcg(kept + d);
-      if (f == d) continue;
-      const int pg = page_of(p.bt, p.c, b, d, p.status, 232);
-      if (pg < 0 || page_of(p.bt, p.c, b, f, p.status, 232) < 0) continue;
-      reinterpret_cast<uint4*>(dst + p.c.row(pg, h, d & p.c.page_mask))[cc] = srow[r * 2 * CH + c];
-    }
-    if (p.c.per_token)
-      for (int r = tid; r < rows; r += ET) {
-        const int d = d0 + r, f = __ldcg(kept + d);
-        if (f == d) continue;
-        const int pg = page_of(p.bt, p.c, b, d, p.status, 232);
-        if (pg < 0 || page_of(p.bt, p.c, b, f, p.status, 232) < 0) continue;
-        const long long si = p.c.scale(pg, h, d & p.c.page_mask);
-        p.c.ks[si] = sscale[r].x;
-        p.c.vs[si] = sscale[r].y;
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      if (f[u] < 0) continue;
+      if ((unsigned)pg[u] >= (unsigned)p.c.pages) {
+        bad(p.status, 232);
+        continue;
       }
-    __syncthreads();  // the staging is free
+      const int slot = (d0 + u * RS) & p.c.page_mask;
+      reinterpret_cast<uint4*>(codes + p.c.row(pg[u], h, slot))[cc] = row[u];
+      if (scales && cc == 0) scales[p.c.scale(pg[u], h, slot)] = scale[u];
+    }
   }
 }
 
@@ -262,7 +278,7 @@ template <int D>
 cudaError_t launch_d(const EvictP& p, cudaStream_t s) {
   auto kern = paged_evict_kernel<D>;
   cudaError_t e;
-  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), STAGE_BYTES)) != cudaSuccess) return e;
+  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), KEY_BYTES)) != cudaSuccess) return e;
   const long long items = (long long)p.bt.B * p.c.H;
   int cs = 8;
   while (cs > 1 && items * cs > sm_count()) cs >>= 1;
@@ -270,7 +286,7 @@ cudaError_t launch_d(const EvictP& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * cs));
   cfg.blockDim = dim3(ET);
-  cfg.dynamicSmemBytes = STAGE_BYTES;
+  cfg.dynamicSmemBytes = KEY_BYTES;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;

@@ -16,29 +16,46 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import _native as N
-from .api import LAYOUTS, MODES, _check, _stream
+from .api import LAYOUTS, MODES, _check
 
 _CODES = {"int8_per_head": torch.int8, "int8_per_token": torch.int8, "fp8_per_head": torch.uint8,
           "fp8_per_token": torch.uint8}
 _PER_HEAD = ("int8_per_head", "fp8_per_head")
 
 
+# a step of a serving loop makes several of these calls, each a few microseconds of GPU time: the checks
+# below are kept to a few attribute reads per tensor
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _here() -> int:
+    """The current device's current stream."""
+    return _raw_stream(_current_device())
+
+
+def _on_device(t: torch.Tensor, what: str):
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if d != _current_device():
+        raise ValueError(f"{what} is not on the current CUDA device")
+
+
 def _dense(t: torch.Tensor, dtype, what: str, shape=None) -> int:
     """The address of a contiguous tensor of that type on the current device, checked."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous {dtype} CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is not on the current CUDA device")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    _on_device(t, what)
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, what: str) -> N.FaRows:
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{what}: expected a bf16 CUDA tensor [T, H, D]")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is not on the current CUDA device")
+    _on_device(t, what)
     T, H, D = t.shape
     st = t.stride()
     if (st[2] != 1 and D > 1) or (st[1] != D and H > 1):
@@ -173,7 +190,7 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, scaling: 
     f, mult = rope_frequencies(rotary_dim, base, scaling)
     out = torch.empty((positions, rotary_dim), dtype=torch.float32, device=device)
     arr = (ctypes.c_double * len(f))(*f)
-    _check(N.lib().fa_rope_table(_dense(out, torch.float32, "table"), positions, rotary_dim, arr, mult, _stream()),
+    _check(N.lib().fa_rope_table(_dense(out, torch.float32, "table"), positions, rotary_dim, arr, mult, _here()),
            "fa_rope_table")
     return out
 
@@ -208,7 +225,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cac
     _check(N.lib().fa_rope_append(ref(tq) if tq is not None else None, ref(tk), ref(tv), ref(cache._c), ref(batch._c), pt,
                                   npos, rd,
                                   None if positions is None else _dense(positions, torch.int32, "positions", (tk.T,)),
-                                  1 if interleaved else 0, am[0], am[1], ref(to) if to is not None else None, _stream()),
+                                  1 if interleaved else 0, am[0], am[1], ref(to) if to is not None else None, _here()),
            "fa_rope_append")
     return out
 
@@ -231,12 +248,12 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, causa
         lse = torch.empty((tq.T, tq.H), dtype=torch.float32, device=q.device)
     need = N.lib().fa_paged_attention_workspace_size(ref(tq), ref(cache._c), ref(batch._c))
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
     _check(N.lib().fa_paged_attention(ref(tq), ref(cache._c), ref(batch._c), 1 if causal else 0, float(softmax_scale),
                                       _dense(out, torch.bfloat16, "out", (tq.T, tq.H, tq.D)),
                                       None if lse is None else _dense(lse, torch.float32, "lse", (tq.T, tq.H)), ws,
-                                      ws_bytes, _stream()), "fa_paged_attention")
+                                      ws_bytes, _here()), "fa_paged_attention")
     return (out, lse) if return_lse else out
 
 
@@ -250,7 +267,7 @@ def paged_weights(q: torch.Tensor, lse: torch.Tensor, cache: PagedCache, batch: 
         raise ValueError(f"acc: expected [{batch.B}, {cache.H}, n]")
     _check(N.lib().fa_paged_weights(ref(tq), _dense(lse, torch.float32, "lse", (tq.T, tq.H)), ref(cache._c), ref(batch._c),
                                     1 if causal else 0, float(softmax_scale), _dense(acc, torch.float32, "acc"),
-                                    acc.shape[2], 1 if accumulate else 0, _stream()), "fa_paged_weights")
+                                    acc.shape[2], 1 if accumulate else 0, _here()), "fa_paged_weights")
     return acc
 
 
@@ -266,9 +283,9 @@ def paged_evict(cache: PagedCache, batch: PagedBatch, scores: torch.Tensor, budg
         raise ValueError("budget must be at least 1")
     ps = _dense(scores, torch.float32, "scores")
     po = None if scores_out is None else _dense(scores_out, torch.float32, "scores_out", scores.shape)
-    kept = torch.empty((batch.B, cache.H, budget), dtype=torch.int32, device=scores.device)
-    new = torch.empty((batch.B,), dtype=torch.int32, device=scores.device)
+    kept = scores.new_empty((batch.B, cache.H, budget), dtype=torch.int32)
+    new = scores.new_empty((batch.B,), dtype=torch.int32)
     _check(N.lib().fa_paged_evict(ctypes.byref(cache._c), ctypes.byref(batch._c), ps, scores.shape[2], int(budget),
-                                  int(sink), int(recent), kept.data_ptr(), new.data_ptr(), po, _stream()),
+                                  int(sink), int(recent), kept.data_ptr(), new.data_ptr(), po, _here()),
            "fa_paged_evict")
     return kept, new

@@ -379,8 +379,8 @@ typedef struct {
 /* Rows of new tokens: bf16 [T, H, D], heads and elements dense, `stride`
  * elements (a multiple of 8, at least H * D) from token to token -- so the q,
  * k and v columns of one fused projection can be passed as they are.  Rows at
- * and past cu_q[B] belong to no sequence (a padded batch): they are not read,
- * and what they would give is left as it was. */
+ * and past cu_q[B] belong to no sequence (a padded batch): what they would
+ * give is left as it was. */
 typedef struct {
   void* data; /* device, bf16, 16-byte aligned */
   int T, H, D;

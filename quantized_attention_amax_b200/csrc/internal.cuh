@@ -179,7 +179,7 @@ cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, const
                               cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s);
 size_t paged_attention_ws(const PagedAttnArgs& a);
-size_t paged_decode_ws();
+size_t paged_decode_ws(int D);
 size_t paged_chunk_ws(int D);
 cudaError_t launch_paged_chunk(const PagedAttnArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int rows, void* ws, cudaStream_t s);

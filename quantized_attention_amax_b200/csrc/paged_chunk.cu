@@ -36,8 +36,7 @@ constexpr float kShift = 7.0f;  // P is held as p 2^7: fp16 keeps 11 bits of it 
 // V scales below this are brought up to it, and their codes (exact otherwise) scaled down: 2^(x - mv) stays finite
 constexpr float kMinScale = 0x1p-90f;
 
-template <bool ALL>
-using CPL = Plan<TN, 2 * BM, ALL ? 1 : 17, 0x7FFFFFFF, true>;
+using CPL = Plan<TN, 2 * BM, 17, 0x7FFFFFFF, true>;
 
 template <int D>
 struct CL {
@@ -152,11 +151,11 @@ __device__ __forceinline__ Piece make_piece(const AttnP& p, const Item& it, long
   return o;
 }
 
-template <int D, bool FP8, bool TOK, bool ALL>
+template <int D, bool FP8, bool TOK>
 __global__ void __launch_bounds__(CT, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnP p) {
   using L = CL<D>;
-  using PL = CPL<ALL>;
+  using PL = CPL;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
@@ -496,12 +495,14 @@ __global__ void __launch_bounds__(CT, 1)
       more = !pc.last;
       int lim;
       float f;
+      bool warp_live;
       {
         // ---- this thread's Q row as fp16, scaled by a power of two
         const Seq s = {pc.q0, pc.m, pc.n};
         const int hk = pc.hk, r = pc.row0 + i + (dual ? 0 : x * BM), ii = r / p.G;
         const bool live = r < s.m * p.G;
         lim = live ? row_limit(p, s, r) : -1;
+        warp_live = __any_sync(0xffffffffu, live);
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride +
                                                           (long long)(hk * p.G + r - ii * p.G) * D);
         float m = 0.0f;
@@ -554,6 +555,16 @@ __global__ void __launch_bounds__(CT, 1)
         }
         if (!(ok = wwait(C_SF + x, n_done, 249))) break;
         tc_fence_after();
+        if (!warp_live) {  // no row of this warp is the sequence's: whatever its P and O are, nothing reads them
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar[C_PF + x]);
+            if (TOK) mbar_arrive(&bar[C_SCE + ss]);
+          }
+          ++n_done;
+          first = false;
+          continue;
+        }
         const bool masked = t * TN + TN - 1 > lim_lo;
         // The row's scores, CW at a time (all 128 at once spill), times s_k in the per-token modes, masked.
         constexpr int CW = 64;
@@ -785,42 +796,42 @@ __global__ void __launch_bounds__(CT, 1)
   }
 }
 
-template <int D, bool FP8, bool TOK, bool ALL>
+template <int D, bool FP8, bool TOK>
 cudaError_t launch_a(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int grid, cudaStream_t s) {
-  auto kern = paged_chunk_kernel<D, FP8, TOK, ALL>;
+  auto kern = paged_chunk_kernel<D, FP8, TOK>;
   cudaError_t e;
   if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), CL<D>::ALLOC)) != cudaSuccess) return e;
   kern<<<grid, CT, CL<D>::ALLOC, s>>>(mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  combine_kernel<CPL<ALL>, D><<<dim3(grid, 8), 128, 0, s>>>(p, grid);
+  combine_kernel<CPL, D><<<dim3(grid, 8), 128, 0, s>>>(p, grid);
   return cudaGetLastError();
 }
 
-template <int D, bool ALL>
+template <int D>
 cudaError_t launch_mode(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int mode, int grid, cudaStream_t s) {
   switch (mode) {
-    case FA_MODE_INT8_PER_HEAD: return launch_a<D, false, false, ALL>(mk, mv, p, grid, s);
-    case FA_MODE_FP8_PER_HEAD: return launch_a<D, true, false, ALL>(mk, mv, p, grid, s);
-    case FA_MODE_INT8_PER_TOKEN: return launch_a<D, false, true, ALL>(mk, mv, p, grid, s);
-    case FA_MODE_FP8_PER_TOKEN: return launch_a<D, true, true, ALL>(mk, mv, p, grid, s);
+    case FA_MODE_INT8_PER_HEAD: return launch_a<D, false, false>(mk, mv, p, grid, s);
+    case FA_MODE_FP8_PER_HEAD: return launch_a<D, true, false>(mk, mv, p, grid, s);
+    case FA_MODE_INT8_PER_TOKEN: return launch_a<D, false, true>(mk, mv, p, grid, s);
+    case FA_MODE_FP8_PER_TOKEN: return launch_a<D, true, true>(mk, mv, p, grid, s);
     default: return cudaErrorNotSupported;
   }
 }
 
 }  // namespace
 
-size_t paged_chunk_ws(int D) { return plan_ws<CPL<false>>(D, sm_count()); }
+size_t paged_chunk_ws(int D) { return plan_ws<CPL>(D, sm_count()); }
 
 cudaError_t launch_paged_chunk(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   AttnP p = paged_attn_params(a);
   const int D = a.q->D, grid = sm_count();
-  plan_carve<CPL<false>>(p, ws, D, grid);
+  plan_carve<CPL>(p, ws, D, grid);
   CUtensorMap mk, mv;
   cudaError_t e;
   if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, 8192 / D, false)) != cudaSuccess) return e;
   if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, 8192 / D, false)) != cudaSuccess) return e;
-  return D == 128 ? launch_mode<128, false>(mk, mv, p, a.cache->mode, grid, s)
-                  : launch_mode<64, true>(mk, mv, p, a.cache->mode, grid, s);
+  return D == 128 ? launch_mode<128>(mk, mv, p, a.cache->mode, grid, s)
+                  : launch_mode<64>(mk, mv, p, a.cache->mode, grid, s);
 }
 
 }  // namespace faq

@@ -1,5 +1,5 @@
 // paged_decode.cu -- attention of at most 16 query rows per kv head (single tokens, drafts) over a paged
-// 8-bit cache, D = 128, on the tensor cores' 8-bit kinds.
+// 8-bit cache, on the tensor cores' 8-bit kinds.
 //
 // The cache's bytes bound it (2 n Hkv D of them per sequence), so nothing but the tensor core touches the
 // codes: TMA brings 128-key tiles of K and V, page by page, into swizzled shared memory, and they are MMA
@@ -7,7 +7,10 @@
 // (paged_digits.cuh), three MMA columns per row:
 //   S^T [128 keys x N] = K . Q^T       A = K codes, B = Q digits,        N >= 3 R (R rows)
 //   O^T [128 dims x N] = V^T . P^T     A = V codes (MN-major), B = P digits
-// A softmax thread owns a key of S^T and a dim of O^T.  Per tile: join the digits' sums into scores, the rows'
+// With D = 64 the second product's 128 rows are the 64 dims over the tile's first 64 keys, then over its last
+// 64 (V's two halves as two operand atoms); its columns are doubled likewise, and of the four blocks the two that
+// pair a half with itself count.
+// A softmax thread owns a key of S^T and a dim of O^T (D = 64: of one half's).  Per tile: join the digits' sums into scores, the rows'
 // maxima over the 128 keys (warp reductions, then the four warps through shared memory), p = 2^(x - m) into the row
 // sums, and the digits of w = p s_v 2^(m - mv) for the second product, mv the running maximum of x + log2 s_v
 // (per-head modes: w = p, mv = m): w is at most 1 whatever the scales' range.  O is kept in registers, rescaled as
@@ -21,30 +24,34 @@ namespace {
 using namespace paged;
 
 constexpr int TK = 128;     // keys per tile
-constexpr int HD = 128;     // head_dim
 constexpr int NST = 3;      // K / V stages
 constexpr int DT = 192;     // warp 0 loads, warp 1 MMAs, warps 2-5 softmax
-constexpr uint32_t TILE = TK * HD;
 
 using DPL = Plan<TK, 16, 1, 16>;
 
-template <int R>
+template <int D, int R>
 struct DL {
   static constexpr int N = R == 4 ? 16 : R == 8 ? 32 : 48;  // 3 R columns, a multiple of 16
+  static constexpr int NO = D == 128 ? N : 2 * N;           // columns of O^T
   static constexpr int NP = R == 16 ? 1 : 2;                // P buffers (16 rows leave room for one)
+  static constexpr int NS = D == 64 && R == 16 ? 1 : 2;     // S buffers (two CTAs share 512 TMEM columns)
+  static constexpr uint32_t TILE = TK * D;
   static constexpr uint32_t K = 0;
   static constexpr uint32_t V = K + NST * TILE;
-  static constexpr uint32_t Q = V + NST * TILE;             // [N][128] digits, 128-byte swizzle
-  static constexpr uint32_t P = Q + N * 128;                // NP x [N][128]
+  static constexpr uint32_t Q = V + NST * TILE;             // [N][D] digits, swizzled
+  static constexpr uint32_t P = Q + N * 128;                // NP x [N][128 keys] (D = 64: [2 N][64 keys])
   static constexpr uint32_t RED = P + NP * N * 128;         // 2 x [4 warps][2 R] maxima
   static constexpr uint32_t SUM = RED + 2 * 4 * 2 * R * 4;  // [4 warps][R] sums
   static constexpr uint32_t ROW = SUM + 4 * R * 4;          // [R] factors, [R] limits
   static constexpr uint32_t BAR = (ROW + 2 * R * 4 + 15) & ~15u;
   static constexpr uint32_t TOTAL = BAR + 256;
   static constexpr uint32_t ALLOC = TOTAL + 1024;
-  static constexpr uint32_t COLS = R == 4 ? 64 : R == 8 ? 128 : 256;  // S and O^T, two buffers each
+  static constexpr uint32_t TO = NS * N;                    // TMEM: S^T buffers, then two of O^T
+  static constexpr uint32_t COLS = TO + 2 * NO <= 64 ? 64 : TO + 2 * NO <= 128 ? 128 : 256;
+  static_assert(TO + 2 * NO <= COLS, "TMEM columns");
   static_assert(Q % 1024 == 0 && (N * 128) % 1024 == 0, "operands keep the swizzle's alignment");
   static_assert(2 * (ALLOC + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(D == 128 || 64 * R * 4 <= N * 128, "the halves' exchange fits a P buffer");
 };
 
 enum {
@@ -91,11 +98,13 @@ struct Run {
   }
 };
 
-template <bool FP8, bool TOK, int R>
+template <int HD, bool FP8, bool TOK, int R>
 __global__ void __launch_bounds__(DT, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnP p) {
-  using L = DL<R>;
-  constexpr int N = L::N;
+  using L = DL<HD, R>;
+  constexpr int N = L::N, NO = L::NO, NS = L::NS;
+  constexpr uint32_t TILE = L::TILE, SW = HD == 128 ? kSwz128 : kSwz64, SBO = 8 * HD;
+  auto swz = [](uint32_t row, uint32_t chunk) { return HD == 128 ? swz128_offset(row, chunk) : swz64_offset(row, chunk); };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
@@ -197,8 +206,8 @@ __global__ void __launch_bounds__(DT, 2)
     if (lane == 0) {
       constexpr uint32_t id_qk = FP8 ? make_idesc(kAccF32, kFmtE4M3, kFmtE4M3, 0, 0, N, 128)
                                      : make_idesc(kAccS32, kFmtS8, kFmtS8, 0, 0, N, 128);
-      constexpr uint32_t id_pv = FP8 ? make_idesc(kAccF32, kFmtE4M3, kFmtE4M3, 1, 0, N, 128)
-                                     : make_idesc(kAccS32, kFmtS8, kFmtU8, 1, 0, N, 128);
+      constexpr uint32_t id_pv = FP8 ? make_idesc(kAccF32, kFmtE4M3, kFmtE4M3, 1, 0, NO, 128)
+                                     : make_idesc(kAccS32, kFmtS8, kFmtU8, 1, 0, NO, 128);
       const uint32_t sQ = smem_u32(smem + L::Q), sK = smem_u32(smem + L::K), sV = smem_u32(smem + L::V), sP = smem_u32(smem + L::P);
       auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
         if (FP8)
@@ -213,9 +222,9 @@ __global__ void __launch_bounds__(DT, 2)
         if (j >= 2 && !mbar_wait(&bar[B_OE + bb], ((j >> 1) - 1) & 1, abort_flag, p.status, 217)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < TK / 32; ++kk)
-          mma(tbase + 2 * N + bb * N, make_sdesc(sV + s * TILE + kk * 32 * HD, 16384, 1024, kSwz128),
-              make_sdesc(sP + (L::NP == 2 ? bb : 0) * N * 128 + kk * 32, 16, 1024, kSwz128), id_pv, kk > 0);
+        for (int kk = 0; kk < HD / 32; ++kk)  // 128 keys, or 64 of both halves (the second operand atom: 64 rows on)
+          mma(tbase + L::TO + bb * NO, make_sdesc(sV + s * TILE + kk * 32 * HD, 64 * HD, SBO, SW),
+              make_sdesc(sP + (L::NP == 2 ? bb : 0) * N * 128 + kk * 32, 16, SBO, SW), id_pv, kk > 0);
         mma_commit(&bar[B_VE + s]);
         mma_commit(&bar[B_OF + bb]);
         return true;
@@ -225,14 +234,14 @@ __global__ void __launch_bounds__(DT, 2)
       do {
         if (run.t0 < run.t1) ok = mbar_wait(&bar[B_Q], piece++ & 1, abort_flag, p.status, 218);
         for (int t = run.t0; t < run.t1 && ok; ++t, ++j) {
-          const int s = j % NST, bb = j & 1;
+          const int s = j % NST, bb = j % NS;
           ok = mbar_wait(&bar[B_KF + s], (j / NST) & 1, abort_flag, p.status, 219) &&
-               (j < 2 || mbar_wait(&bar[B_SE + bb], ((j >> 1) - 1) & 1, abort_flag, p.status, 220));
+               (j < NS || mbar_wait(&bar[B_SE + bb], (j / NS - 1) & 1, abort_flag, p.status, 220));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < HD / 32; ++kk)
-            mma(tbase + bb * N, make_sdesc(sK + s * TILE + kk * 32, 16, 1024, kSwz128), make_sdesc(sQ + kk * 32, 16, 1024, kSwz128),
+            mma(tbase + bb * N, make_sdesc(sK + s * TILE + kk * 32, 16, SBO, SW), make_sdesc(sQ + kk * 32, 16, SBO, SW),
                 id_qk, kk > 0);
           mma_commit(&bar[B_KE + s]);
           mma_commit(&bar[B_SF + bb]);
@@ -248,10 +257,12 @@ __global__ void __launch_bounds__(DT, 2)
   } else {
     // ---------------------------------------------------------------- softmax
     const int wg = warp & 3;          // TMEM lanes 32 wg .. + 31
-    const int i = wg * 32 + lane;     // key of S^T, dim of O^T
+    const int i = wg * 32 + lane;     // key of S^T, row of O^T: dim i, or (D = 64) dim i % 64 over half i / 64 of the keys
+    const int half = HD == 128 ? 0 : wg >> 1;
     const uint32_t loff = (uint32_t)(wg * 32) << 16;
     float* red = reinterpret_cast<float*>(smem + L::RED);
     float* sums = reinterpret_cast<float*>(smem + L::SUM);
+    float* halves = reinterpret_cast<float*>(smem + L::P);  // at a piece's end, when no P is in use
     float* rowf = reinterpret_cast<float*>(smem + L::ROW);
     int* rowl = reinterpret_cast<int*>(smem + L::ROW) + R;
     auto wait = [&](int which, int phase, int where) {
@@ -270,10 +281,11 @@ __global__ void __launch_bounds__(DT, 2)
         al_o[r] = 1.0f;
       }
       if (run.t0 < run.t1) {
-        // ---- Q digits: eight lanes a row, 16 values each
-        for (int idx = i; idx < R * 8; idx += 128) {
-          const int r = idx >> 3, c = idx & 7, ii = r / p.G;
-          const bool live = r < rows;
+        // ---- Q digits: D / 16 lanes a row, 16 values each
+        constexpr int LPR = HD / 16;
+        for (int idx = i; idx - lane < R * LPR; idx += 128) {
+          const int r = idx / LPR, c = idx % LPR, ii = r / p.G;
+          const bool live = r < R && r < rows;
           const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride +
                                                             (long long)(hk * p.G + r - ii * p.G) * HD + c * 16);
           uint4 raw[2];
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(DT, 2)
           }
           if (bad_value) m = INFINITY;
 #pragma unroll
-          for (int off = 4; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          for (int off = LPR / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
           float inv;
           const float sc = digit_scale<FP8>(m, inv);
           uint32_t dw[3][4] = {};
@@ -303,9 +315,10 @@ __global__ void __launch_bounds__(DT, 2)
 #pragma unroll
             for (int k = 0; k < 3; ++k) dw[k][e >> 2] |= d[k] << (8 * (e & 3));
           }
+          if (r >= R) continue;
 #pragma unroll
           for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint4*>(smem + L::Q + swz128_offset(k * R + r, c)) =
+            *reinterpret_cast<uint4*>(smem + L::Q + swz(k * R + r, c)) =
                 make_uint4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
           if (c == 0) {
             rowf[r] = p.scale_log2 * inv * (TOK ? 1.0f : __ldg(p.c.ks + hk));
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(DT, 2)
         pg_n = load_page(run.t0 + 1);
       }
       for (int t = run.t0; t < run.t1 && ok; ++t, ++j) {
-        const int bb = j & 1;
+        const int bb = j & 1, sb = j % NS;
         const int key = t * TK + i;
         const bool masked = t * TK + TK - 1 > lim_lo;
         if (TOK) {
@@ -368,15 +381,15 @@ __global__ void __launch_bounds__(DT, 2)
           }
           v_bad = v_bad || (nan && key < s.n);
         }
-        if (!(ok = wait(B_SF + bb, j >> 1, 223))) break;
+        if (!(ok = wait(B_SF + sb, j / NS, 223))) break;
         tc_fence_after();
         uint32_t a[N];
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) tmem_ld16(tbase + bb * N + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
+        for (int c = 0; c < N / 16; ++c) tmem_ld16(tbase + sb * N + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[B_SE + bb]);
+        if (lane == 0) mbar_arrive(&bar[B_SE + sb]);
         // ---- scores and the rows' maxima
         float x[R];
         const float lsv = TOK ? log2f(v_bad ? 0.0f : sv) : 0.0f;
@@ -427,7 +440,7 @@ __global__ void __launch_bounds__(DT, 2)
           uint32_t d[3];
           p_digits<FP8>(w, d);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) sp[swz128_offset(k * R + r, i >> 4) + (i & 15)] = (uint8_t)d[k];
+          for (int k = 0; k < 3; ++k) sp[swz((HD == 128 ? 0 : (i >> 6) * N) + k * R + r, (HD == 128 ? i : i & 63) >> 4) + (i & 15)] = (uint8_t)d[k];
         }
         fence_async_smem();
         __syncwarp();
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(DT, 2)
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < N / 16; ++c)
-            tmem_ld16(tbase + 2 * N + jb * N + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
+            tmem_ld16(tbase + L::TO + jb * NO + half * N + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -459,7 +472,7 @@ __global__ void __launch_bounds__(DT, 2)
         uint32_t a[N];
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
-          tmem_ld16(tbase + 2 * N + jb * N + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
+          tmem_ld16(tbase + L::TO + jb * NO + half * N + c * 16 + loff, *reinterpret_cast<uint32_t(*)[16]>(&a[16 * c]));
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
@@ -471,18 +484,22 @@ __global__ void __launch_bounds__(DT, 2)
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
           if (lane == 0) sums[wg * R + r] = l;
+          if (HD == 64 && half) halves[r * 64 + (i & 63)] = o[r];
         }
         mbar_arrive(&bar[B_SUM]);
         if (!(ok = wait(B_SUM, piece, 228))) break;
         ++piece;
 #pragma unroll
-        for (int r = 0; r < R; ++r) l_run[r] = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
+        for (int r = 0; r < R; ++r) {
+          if (HD == 64 && !half) o[r] += halves[r * 64 + i];
+          l_run[r] = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
+        }
       }
       const bool whole = run.u == run.it.first && run.it.first + run.it.nt <= run.u1;
       const int slot = 2 * blockIdx.x + (run.u == run.u0 ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= rows) break;
+        if (r >= rows || half) break;
         const float val = o[r] * kPUnit<FP8>;
         if (whole) {
           const int ii = r / p.G;
@@ -505,43 +522,50 @@ __global__ void __launch_bounds__(DT, 2)
   }
 }
 
-template <bool FP8, bool TOK, int R>
+template <int D, bool FP8, bool TOK, int R>
 cudaError_t launch_r(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int grid, cudaStream_t s) {
-  auto kern = paged_decode_kernel<FP8, TOK, R>;
+  auto kern = paged_decode_kernel<D, FP8, TOK, R>;
   cudaError_t e;
-  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), DL<R>::ALLOC)) != cudaSuccess) return e;
-  kern<<<grid, DT, DL<R>::ALLOC, s>>>(mk, mv, p);
+  if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), DL<D, R>::ALLOC)) != cudaSuccess) return e;
+  kern<<<grid, DT, DL<D, R>::ALLOC, s>>>(mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  combine_kernel<DPL, HD><<<grid, 128, 0, s>>>(p, grid);
+  combine_kernel<DPL, D><<<grid, 128, 0, s>>>(p, grid);
   return cudaGetLastError();
 }
 
-template <bool FP8, bool TOK>
-cudaError_t launch_mode(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int rows, int grid, cudaStream_t s) {
-  if (rows <= 4) return launch_r<FP8, TOK, 4>(mk, mv, p, grid, s);
-  if (rows <= 8) return launch_r<FP8, TOK, 8>(mk, mv, p, grid, s);
-  return launch_r<FP8, TOK, 16>(mk, mv, p, grid, s);
+template <int D, bool FP8, bool TOK>
+cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int rows, int grid, cudaStream_t s) {
+  if (rows <= 4) return launch_r<D, FP8, TOK, 4>(mk, mv, p, grid, s);
+  if (rows <= 8) return launch_r<D, FP8, TOK, 8>(mk, mv, p, grid, s);
+  return launch_r<D, FP8, TOK, 16>(mk, mv, p, grid, s);
+}
+
+template <int D>
+cudaError_t launch_mode(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& p, int mode, int rows, int grid,
+                        cudaStream_t s) {
+  switch (mode) {
+    case FA_MODE_INT8_PER_HEAD: return launch_rows<D, false, false>(mk, mv, p, rows, grid, s);
+    case FA_MODE_FP8_PER_HEAD: return launch_rows<D, true, false>(mk, mv, p, rows, grid, s);
+    case FA_MODE_INT8_PER_TOKEN: return launch_rows<D, false, true>(mk, mv, p, rows, grid, s);
+    case FA_MODE_FP8_PER_TOKEN: return launch_rows<D, true, true>(mk, mv, p, rows, grid, s);
+    default: return cudaErrorNotSupported;
+  }
 }
 
 }  // namespace
 
-size_t paged_decode_ws() { return plan_ws<DPL>(HD, 2 * sm_count()); }
+size_t paged_decode_ws(int D) { return plan_ws<DPL>(D, 2 * sm_count()); }
 
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int rows, void* ws, cudaStream_t s) {
   AttnP p = paged_attn_params(a);
-  const int grid = 2 * sm_count();
-  plan_carve<DPL>(p, ws, HD, grid);
+  const int D = a.q->D, grid = 2 * sm_count();
+  plan_carve<DPL>(p, ws, D, grid);
   CUtensorMap mk, mv;
   cudaError_t e;
   if ((e = make_page_map(&mk, a.cache->k_codes, *a.cache, TK, true)) != cudaSuccess) return e;
   if ((e = make_page_map(&mv, a.cache->v_codes, *a.cache, TK, true)) != cudaSuccess) return e;
-  switch (a.cache->mode) {
-    case FA_MODE_INT8_PER_HEAD: return launch_mode<false, false>(mk, mv, p, rows, grid, s);
-    case FA_MODE_FP8_PER_HEAD: return launch_mode<true, false>(mk, mv, p, rows, grid, s);
-    case FA_MODE_INT8_PER_TOKEN: return launch_mode<false, true>(mk, mv, p, rows, grid, s);
-    case FA_MODE_FP8_PER_TOKEN: return launch_mode<true, true>(mk, mv, p, rows, grid, s);
-    default: return cudaErrorNotSupported;
-  }
+  return D == 128 ? launch_mode<128>(mk, mv, p, a.cache->mode, rows, grid, s)
+                  : launch_mode<64>(mk, mv, p, a.cache->mode, rows, grid, s);
 }
 
 }  // namespace faq

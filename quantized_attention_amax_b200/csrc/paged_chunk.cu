@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(CT, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  let_next_start();
   auto wait = [&](int which, int phase, int where) { return mbar_wait(&bar[which], phase & 1, abort_flag, p.status, where); };
   auto wwait = [&](int which, int phase, int where) { return __all_sync(0xffffffffu, wait(which, phase, where)); };
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::PC);
@@ -803,8 +804,7 @@ cudaError_t launch_a(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& 
   if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), CL<D>::ALLOC)) != cudaSuccess) return e;
   kern<<<grid, CT, CL<D>::ALLOC, s>>>(mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  combine_kernel<CPL, D><<<dim3(grid, 8), 128, 0, s>>>(p, grid);
-  return cudaGetLastError();
+  return launch_combine<CPL, D>(p, grid, s);
 }
 
 template <int D>

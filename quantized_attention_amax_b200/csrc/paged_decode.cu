@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(DT, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  let_next_start();
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
@@ -529,8 +530,7 @@ cudaError_t launch_r(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP& 
   if ((e = set_smem_limit(reinterpret_cast<const void*>(kern), DL<D, R>::ALLOC)) != cudaSuccess) return e;
   kern<<<grid, DT, DL<D, R>::ALLOC, s>>>(mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  combine_kernel<DPL, D><<<grid, 128, 0, s>>>(p, grid);
-  return cudaGetLastError();
+  return launch_combine<DPL, D>(p, grid, s);
 }
 
 template <int D, bool FP8, bool TOK>

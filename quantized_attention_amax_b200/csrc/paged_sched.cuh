@@ -190,10 +190,19 @@ __device__ __forceinline__ float row_factor(const AttnP& p, int hk, float l, flo
 }
 __device__ __forceinline__ float row_lse(float l, float m) { return (m + log2f(l)) * 0.69314718055994530942f; }
 
+// Programmatic dependent launch: a kernel lets the one behind it start (its launch and prologue then overlap), which
+// waits for it before reading what it wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The merge of the items that a run's border cuts: CTA c takes the item that starts in run c and
-// ends past it, whose pieces lie in run c's slot and in slot 0 of the runs after it.
+// ends past it, whose pieces lie in run c's slot and in slot 0 of the runs after it; blockIdx.y takes 16 of the
+// block's rows.  A thread holds four dims of one or two rows.  The pieces' (m, l, mv) come through shared memory,
+// CB at a time, so that the loads of the accumulators do not wait for one another (one piece after
+// another took 32 us for the 38 pieces of a 131071-token item; this 5).
+constexpr int CB = 64;
 template <typename PL, int D>
-__global__ void __launch_bounds__(128) combine_kernel(const AttnP p, int grid) {
+__global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x;
   const long long total = total_units<PL>(p, lane);
@@ -204,43 +213,107 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnP p, int grid) {
   const Item it = find_item<PL>(p, u1 - 1, lane);
   const long long item_end = it.first + it.nt;
   if (item_end <= u1 || it.first < u0) return;
-  int last = c + 1;
-  while (run_start(total, last + 1, runs) < item_end) ++last;
-  const int slot0 = 2 * c + (it.first == u0 ? 0 : 1);
-  const int rows = min(it.s.m * p.G - it.rb * PL::RB, PL::RB);
-  // several CTAs (blockIdx.y) share a block's rows
-  for (int idx = blockIdx.y * blockDim.x + threadIdx.x; idx < rows * (D / 4); idx += gridDim.y * blockDim.x) {
-    const int r = idx / (D / 4), ch = idx % (D / 4);
-    float m = -INFINITY, mv = -INFINITY;
-    for (int k = c; k <= last; ++k) {
-      const float4 v = __ldg(p.part_ml + (long long)(k == c ? slot0 : 2 * k) * PL::RB + r);
-      m = fmaxf(m, v.x);
-      mv = fmaxf(mv, v.z);
-    }
-    float l = 0.0f;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = c; k <= last; ++k) {
-      const long long row = (long long)(k == c ? slot0 : 2 * k) * PL::RB + r;
-      const float4 v = __ldg(p.part_ml + row);
-      if (v.x > -INFINITY) l += attn::ex2(v.x - m) * v.y;
-      if (v.z > -INFINITY) {
-        const float w = attn::ex2(v.z - mv);
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_o + row * D) + ch);
-        a.x += w * x.x;
-        a.y += w * x.y;
-        a.z += w * x.z;
-        a.w += w * x.w;
+  const int row0 = blockIdx.y * 16, rows = min(it.s.m * p.G - it.rb * PL::RB, PL::RB);
+  if (row0 >= rows) return;
+  // the run that holds the item's last unit u: the largest k with floor(total k / runs) <= u
+  const int last = (int)((item_end * runs - 1) / total);
+  const int pieces = last - c + 1, slot0 = 2 * c + (it.first == u0 ? 0 : 1);
+  wait_for_previous();
+  constexpr int CPR = D / 4, RT = 256 / CPR, NR = 16 / RT;  // chunks a row, rows side by side, rows a thread
+  const int ch = threadIdx.x % CPR, rid = threadIdx.x / CPR;
+  // few rows: the threads that would have none share the pieces out
+  const int left = rows - row0;
+  const int across = left > 4 ? RT : left > 2 ? min(4, RT) : left > 1 ? 2 : 1, splits = RT / across;
+  const int r0 = rid % across, part = rid / across;
+  __shared__ float4 ml[CB][16];
+  __shared__ float4 sum[256];
+  __shared__ float sum_l[256];
+  float m[NR], mv[NR], l[NR];
+  float4 acc[NR];
+#pragma unroll
+  for (int y = 0; y < NR; ++y) {
+    m[y] = mv[y] = -INFINITY;
+    l[y] = 0.0f;
+    acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  auto row_of = [&](int k, int r) { return (long long)(k == 0 ? slot0 : 2 * (c + k)) * PL::RB + row0 + r; };
+  for (int k0 = 0; k0 < pieces; k0 += CB) {
+    const int n = min(CB, pieces - k0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * 16; i += 256) ml[i / 16][i % 16] = p.part_ml[row_of(k0 + i / 16, i % 16)];
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+      const int r = r0 + y * RT;
+      if (row0 + r >= rows || (y > 0 && splits > 1)) continue;
+      float mn = m[y], mvn = mv[y];
+      for (int k = 0; k < n; ++k) {
+        mn = fmaxf(mn, ml[k][r].x);
+        mvn = fmaxf(mvn, ml[k][r].z);
+      }
+      const float wl = mn == m[y] ? 1.0f : attn::ex2(m[y] - mn), wo = mvn == mv[y] ? 1.0f : attn::ex2(mv[y] - mvn);
+      l[y] *= wl;  // (every part sees every piece's maxima)
+      acc[y] = make_float4(acc[y].x * wo, acc[y].y * wo, acc[y].z * wo, acc[y].w * wo);
+      m[y] = mn;
+      mv[y] = mvn;
+#pragma unroll 8
+      for (int k = part; k < n; k += splits) {
+        const float4 v = ml[k][r];
+        const float4 x = *(reinterpret_cast<const float4*>(p.part_o + row_of(k0 + k, r) * D) + ch);
+        if (v.x > -INFINITY) l[y] += attn::ex2(v.x - mn) * v.y;
+        const float w = v.z > -INFINITY ? attn::ex2(v.z - mvn) : 0.0f;
+        if (w != 0.0f) {  // a piece without weight may hold anything
+          acc[y].x += w * x.x;
+          acc[y].y += w * x.y;
+          acc[y].z += w * x.z;
+          acc[y].w += w * x.w;
+        }
       }
     }
-    const int rr = it.rb * PL::RB + r;
+  }
+  if (splits > 1) {
+    sum[threadIdx.x] = acc[0];
+    sum_l[threadIdx.x] = l[0];
+    __syncthreads();
+    if (part > 0) return;
+    for (int q = 1; q < splits; ++q) {
+      const int t = threadIdx.x + q * across * CPR;
+      const float4 x = sum[t];
+      acc[0].x += x.x;
+      acc[0].y += x.y;
+      acc[0].z += x.z;
+      acc[0].w += x.w;
+      l[0] += sum_l[t];
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < NR; ++y) {
+    const int r = r0 + y * RT;
+    if (row0 + r >= rows || (y > 0 && splits > 1)) continue;
+    const int rr = it.rb * PL::RB + row0 + r;
     const int i = rr / p.G, hq = it.hk * p.G + rr - i * p.G;
-    const float f = row_factor(p, it.hk, l, m, mv);
+    const float f = row_factor(p, it.hk, l[y], m[y], mv[y]);
     const long long row = (long long)(it.s.q0 + i) * p.Hq + hq;
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(a.x * f, a.y * f), v1 = __floats2bfloat162_rn(a.z * f, a.w * f);
+    const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[y].x * f, acc[y].y * f), v1 = __floats2bfloat162_rn(acc[y].z * f, acc[y].w * f);
     *reinterpret_cast<uint2*>(p.out + row * D + ch * 4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
-    if (ch == 0 && p.lse) p.lse[row] = row_lse(l, m);
+    if (ch == 0 && p.lse) p.lse[row] = row_lse(l[y], m[y]);
   }
+}
+
+// The combine kernel behind a kernel of that plan that let it start.
+template <typename PL, int D>
+inline cudaError_t launch_combine(const AttnP& p, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, PL::RB / 16);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<PL, D>, p, grid);
 }
 
 // Workspace of a kernel of that plan with `grid` CTAs.

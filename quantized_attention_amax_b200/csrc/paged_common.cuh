@@ -1,5 +1,5 @@
 // paged_common.cuh -- what the paged-cache kernels share: the cache and batch as kernels see them,
-// the checks of lengths and pages, and the 8-bit code conversions and 16-bit MMAs on registers.
+// the checks of lengths and pages, and the conversions of 8-bit codes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -74,27 +74,6 @@ __device__ __forceinline__ int page_of(const Batch& bt, const Cache& c, int b, i
     return -1;
   }
   return pg;
-}
-
-// 16 bytes global -> shared, asynchronously; zeros where !ok (the source is then not read).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// D (16 x 8, fp32) += A (16 x 16, fp16) * B (16 x 8, fp16) on one warp's registers.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Four codes of one word -> two fp16 pairs (bytes 0, 1 and 2, 3), exactly.

@@ -207,18 +207,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
   const int c = blockIdx.x;
   const long long total = total_units<PL>(p, lane);
   const int runs = run_count(total, grid);
-  if (c >= runs) return;
-  const long long u0 = run_start(total, c, runs), u1 = run_start(total, c + 1, runs);
-  if (u1 >= total) return;
-  const Item it = find_item<PL>(p, u1 - 1, lane);
-  const long long item_end = it.first + it.nt;
-  if (item_end <= u1 || it.first < u0) return;
-  const int row0 = blockIdx.y * 16, rows = min(it.s.m * p.G - it.rb * PL::RB, PL::RB);
+  Item it = {};
+  long long item_end = 0;
+  int rows = 0, slot0 = 0;
+  const int row0 = blockIdx.y * 16;
+  if (c < runs) {
+    const long long u0 = run_start(total, c, runs), u1 = run_start(total, c + 1, runs);
+    if (u1 < total) {
+      it = find_item<PL>(p, u1 - 1, lane);
+      item_end = it.first + it.nt;
+      if (item_end > u1 && it.first >= u0) rows = min(it.s.m * p.G - it.rb * PL::RB, PL::RB);
+      slot0 = 2 * c + (it.first == u0 ? 0 : 1);
+    }
+  }
+  // Every CTA waits, those without work too: what follows this kernel in the stream then follows the one before it.
+  wait_for_previous();
   if (row0 >= rows) return;
   // the run that holds the item's last unit u: the largest k with floor(total k / runs) <= u
   const int last = (int)((item_end * runs - 1) / total);
-  const int pieces = last - c + 1, slot0 = 2 * c + (it.first == u0 ? 0 : 1);
-  wait_for_previous();
+  const int pieces = last - c + 1;
   constexpr int CPR = D / 4, RT = 256 / CPR, NR = 16 / RT;  // chunks a row, rows side by side, rows a thread
   const int ch = threadIdx.x % CPR, rid = threadIdx.x / CPR;
   // few rows: the threads that would have none share the pieces out

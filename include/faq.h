@@ -413,8 +413,8 @@ FAQ_API fa_status fa_rope_table(float* table, int positions, int rotary_dim, con
  *   K (rotated, bf16) and V are quantized as fa_quantize does in the cache's
  *   mode and stored at the tokens' cache indices; in the per-token modes a
  *   row holding a NaN gets a NaN scale and zero codes.  The per-head modes
- *   need amax_k, amax_v (device fp32 [H], FA_ERR_NO_CALIBRATION if NULL) and
- *   (re)write the cache's scales with amax / 127 or amax / 448.
+ *   need amax_k, amax_v (device fp32 [H], FA_ERR_NO_CALIBRATION if NULL) and,
+ *   with T > 0, (re)write the cache's scales with amax / 127 or amax / 448.
  *   q, q_out: rows of one T, H and D; q_out may be q (in place).  Both NULL:
  *   K and V only.  A page written by this call must not be another
  *   sequence's page too.
@@ -437,15 +437,22 @@ FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_ro
  *   workspace: fa_paged_attention_workspace_size() bytes, 256-byte aligned
  *   (FA_ERR_WORKSPACE otherwise); only used during the call's kernels, so
  *   calls that can overlap (two streams) need one each.
- *   Scores, maxima, sums and accumulators are fp32; the probabilities enter
- *   the second product as fp16.
+ *   out must not overlap q.
+ *   Scores, maxima, sums and accumulators are fp32.  Sequences of at most 16
+ *   query rows per kv head (m_b * Hq / Hkv): Q and the probabilities enter the
+ *   products as sums of three 8-bit terms (INT8: 24-bit integers of the row's
+ *   range; E4M3: at least 12 bits); more rows: Q as fp16 times a power of two
+ *   per row (bf16 values exact down to 2^-29 of the row's largest), the
+ *   probabilities as fp16.  A NaN E4M3 code, or a scale that is NaN or
+ *   infinite, makes the rows that see its token NaN and no others.
  */
 FAQ_API fa_status fa_paged_attention(const fa_rows* q, const fa_paged_cache* cache, const fa_paged_batch* batch,
                                      int causal, float softmax_scale, void* out, float* lse, void* workspace,
                                      size_t ws_bytes, fa_stream_t s);
 
-/* Workspace bytes of fa_paged_attention for these operands (it does not grow
- * with the cached lengths).  Returns 0 on invalid arguments. */
+/* Workspace bytes of fa_paged_attention for these operands (by head sizes and
+ * batch->max_q; it does not grow with the cached lengths).  Returns 0 on
+ * invalid arguments. */
 FAQ_API size_t fa_paged_attention_workspace_size(const fa_rows* q, const fa_paged_cache* cache,
                                                  const fa_paged_batch* batch);
 
@@ -480,7 +487,7 @@ FAQ_API fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_
  *   kept tokens' scores in order, then 0.  batch->cu_q is not used.  Keys
  *   keep the rotation of their first positions, so later tokens need explicit
  *   positions in fa_rope_append.  A page must not be in two sequences.
- *   budget >= 1, sink + recent <= budget.
+ *   budget: 1 to 2^30 (above: FA_ERR_UNSUPPORTED); sink + recent <= budget.
  */
 FAQ_API fa_status fa_paged_evict(const fa_paged_cache* cache, const fa_paged_batch* batch, const float* scores,
                                  long long score_stride, int budget, int sink, int recent, int* kept, int* new_lens,

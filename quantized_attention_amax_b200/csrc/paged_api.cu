@@ -136,8 +136,8 @@ fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_paged_ca
   const fa_status st = check_attend(q, cache, batch);
   if (st != FA_OK) return st;
   if (acc_stride < 0) return FA_ERR_INVALID_ARG;
-  if (q->T == 0 || batch->B == 0) return FA_OK;
-  if (!lse || !aligned(lse, 4) || !acc || !aligned(acc, 4)) return FA_ERR_INVALID_ARG;
+  if (batch->B == 0 || (q->T == 0 && accumulate)) return FA_OK;  // (no new token: the weights are zero)
+  if ((q->T > 0 && !lse) || !aligned(lse, 4) || (acc_stride > 0 && !acc) || !aligned(acc, 4)) return FA_ERR_INVALID_ARG;
   int* status = device_status_ptr();
   if (!status) return FA_ERR_CUDA;
   const PagedAttnArgs a = {q,   cache, batch,      causal ? 1 : 0, softmax_scale, nullptr, const_cast<float*>(lse), status,
@@ -153,10 +153,11 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const fa_paged_batch* batc
   if ((st = check_batch(batch)) != FA_OK) return st;
   if (score_stride < 0 || budget < 1 || sink < 0 || recent < 0 || (long long)sink + recent > budget)
     return FA_ERR_INVALID_ARG;
-  if (!lengths_fit(cache, batch)) return FA_ERR_UNSUPPORTED;
+  // (a budget near 2^31 would pass 32 bits in the loops over its entries)
+  if (!lengths_fit(cache, batch) || budget > 0x40000000) return FA_ERR_UNSUPPORTED;
   if (batch->B == 0) return FA_OK;
-  if (!scores || !aligned(scores, 4) || !kept || !aligned(kept, 4) || !new_lens || !aligned(new_lens, 4) ||
-      !aligned(scores_out, 4) || scores == scores_out)
+  if ((score_stride > 0 && !scores) || !aligned(scores, 4) || !kept || !aligned(kept, 4) || !new_lens ||
+      !aligned(new_lens, 4) || !aligned(scores_out, 4) || (scores && scores == scores_out))
     return FA_ERR_INVALID_ARG;
   int* status = device_status_ptr();
   if (!status) return FA_ERR_CUDA;

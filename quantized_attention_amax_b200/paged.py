@@ -52,6 +52,14 @@ def _dense(t: torch.Tensor, dtype, what: str, shape=None) -> int:
     return t.data_ptr()
 
 
+def _int32(x, what: str) -> int:
+    """x as the C interface takes it: what does not fit would wrap there."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{what} must fit 32 bits, got {x}")
+    return x
+
+
 def _rows(t: torch.Tensor, what: str) -> N.FaRows:
     if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{what}: expected a bf16 CUDA tensor [T, H, D]")
@@ -63,11 +71,12 @@ def _rows(t: torch.Tensor, what: str) -> N.FaRows:
     return N.FaRows(t.data_ptr(), T, H, D, st[0] if T > 1 else H * D)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class PagedCache:
     """Pages of quantized K and V (fa_paged_cache): codes [pages, H, page_size, D] (layout "BNSD") or
     [pages, page_size, H, D] ("BSND"), int8 or E4M3 bytes (uint8); scales fp32 [H] in the per-head
-    modes, [pages, H, page_size] in the per-token ones."""
+    modes, [pages, H, page_size] in the per-token ones.  Its tensors are the ones it was made with: write
+    into them, or make another for other tensors."""
     k_codes: torch.Tensor
     v_codes: torch.Tensor
     k_scales: torch.Tensor
@@ -83,24 +92,32 @@ class PagedCache:
         s = self.k_codes.shape
         if len(s) != 4:
             raise ValueError("codes: expected 4 dimensions")
-        self.pages, self.D = s[0], s[3]
-        self.H, self.page_size = (s[1], s[2]) if self.layout == "BNSD" else (s[2], s[1])
+        put = lambda name, value: object.__setattr__(self, name, value)
+        put("pages", s[0])
+        put("D", s[3])
+        put("H", s[1] if self.layout == "BNSD" else s[2])
+        put("page_size", s[2] if self.layout == "BNSD" else s[1])
         sc = (self.H,) if self.mode in _PER_HEAD else (self.pages, self.H, self.page_size)
         dt = _CODES[self.mode]
-        self._c = N.FaPagedCache(_dense(self.k_codes, dt, "k_codes"), _dense(self.v_codes, dt, "v_codes", s),
+        put("_c", N.FaPagedCache(_dense(self.k_codes, dt, "k_codes"), _dense(self.v_codes, dt, "v_codes", s),
                                  _dense(self.k_scales, torch.float32, "k_scales", sc),
                                  _dense(self.v_scales, torch.float32, "v_scales", sc), MODES[self.mode], self.pages,
-                                 self.H, self.page_size, self.D, LAYOUTS[self.layout])
+                                 self.H, self.page_size, self.D, LAYOUTS[self.layout]))
+        put("_device", _current_device())
 
     def c(self) -> N.FaPagedCache:
+        """The descriptor, for a call on the current device."""
+        if self._device != _current_device():
+            raise ValueError("the cache is not on the current CUDA device")
         return self._c
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class PagedBatch:
     """The sequences of one call (fa_paged_batch): page_table int32 [B, max_pages]; seq_lens int32 [B],
     cached tokens with the new ones; cu_q int32 [B + 1], the new tokens' row offsets (None: one new
-    token per sequence); max_q, a bound on a sequence's new tokens (0: all rows)."""
+    token per sequence); max_q, a bound on a sequence's new tokens (0: all rows).  Its tensors are the ones it
+    was made with: write into them (a captured graph then follows), or make another for other tensors."""
     page_table: torch.Tensor
     seq_lens: torch.Tensor
     cu_q: Optional[torch.Tensor] = None
@@ -110,13 +127,18 @@ class PagedBatch:
         if self.page_table.dim() != 2:
             raise ValueError("page_table: expected [B, max_pages]")
         B, wide = self.page_table.shape
-        self.B = B
-        self._c = N.FaPagedBatch(_dense(self.page_table, torch.int32, "page_table"),
+        put = lambda name, value: object.__setattr__(self, name, value)
+        put("B", B)
+        put("_c", N.FaPagedBatch(_dense(self.page_table, torch.int32, "page_table"),
                                  _dense(self.seq_lens, torch.int32, "seq_lens", (B,)),
                                  None if self.cu_q is None else _dense(self.cu_q, torch.int32, "cu_q", (B + 1,)), B, wide,
-                                 int(self.max_q))
+                                 _int32(self.max_q, "max_q")))
+        put("_device", _current_device())
 
     def c(self) -> N.FaPagedBatch:
+        """The descriptor, for a call on the current device."""
+        if self._device != _current_device():
+            raise ValueError("the batch is not on the current CUDA device")
         return self._c
 
 
@@ -222,7 +244,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cac
     if amax is not None:
         am = tuple(_dense(a, torch.float32, "amax", (cache.H,)) for a in amax)
     ref = ctypes.byref
-    _check(N.lib().fa_rope_append(ref(tq) if tq is not None else None, ref(tk), ref(tv), ref(cache._c), ref(batch._c), pt,
+    _check(N.lib().fa_rope_append(ref(tq) if tq is not None else None, ref(tk), ref(tv), ref(cache.c()), ref(batch.c()), pt,
                                   npos, rd,
                                   None if positions is None else _dense(positions, torch.int32, "positions", (tk.T,)),
                                   1 if interleaved else 0, am[0], am[1], ref(to) if to is not None else None, _here()),
@@ -232,25 +254,31 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cac
 
 def paged_attention_workspace_size(q: torch.Tensor, cache: PagedCache, batch: PagedBatch) -> int:
     tq = _rows(q, "q")
-    return int(N.lib().fa_paged_attention_workspace_size(ctypes.byref(tq), ctypes.byref(cache._c), ctypes.byref(batch._c)))
+    return int(N.lib().fa_paged_attention_workspace_size(ctypes.byref(tq), ctypes.byref(cache.c()), ctypes.byref(batch.c())))
 
 
 def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, causal: bool = True,
                     softmax_scale: float = 0.0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                     return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
     """Attention of the new tokens q [T, Hq, D] over the cache (fa_paged_attention), bf16 [T, Hq, D].
-    Returns out, or (out, lse) with return_lse (lse fp32 [T, Hq])."""
+    Returns out, or (out, lse) with return_lse (lse fp32 [T, Hq]).  ``workspace``: bytes to use where it is
+    large enough (paged_attention_workspace_size), else it is allocated."""
     tq = _rows(q, "q")
     ref = ctypes.byref
     if out is None:
         out = torch.empty((tq.T, tq.H, tq.D), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((tq.T, tq.H), dtype=torch.float32, device=q.device)
-    need = N.lib().fa_paged_attention_workspace_size(ref(tq), ref(cache._c), ref(batch._c))
+    c, b = ref(cache.c()), ref(batch.c())
+    if workspace is not None:
+        _on_device(workspace, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor")
+    need = N.lib().fa_paged_attention_workspace_size(ref(tq), c, b)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = q.new_empty(need, dtype=torch.uint8)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
-    _check(N.lib().fa_paged_attention(ref(tq), ref(cache._c), ref(batch._c), 1 if causal else 0, float(softmax_scale),
+    _check(N.lib().fa_paged_attention(ref(tq), c, b, 1 if causal else 0, float(softmax_scale),
                                       _dense(out, torch.bfloat16, "out", (tq.T, tq.H, tq.D)),
                                       None if lse is None else _dense(lse, torch.float32, "lse", (tq.T, tq.H)), ws,
                                       ws_bytes, _here()), "fa_paged_attention")
@@ -265,7 +293,7 @@ def paged_weights(q: torch.Tensor, lse: torch.Tensor, cache: PagedCache, batch: 
     ref = ctypes.byref
     if acc.dim() != 3 or tuple(acc.shape[:2]) != (batch.B, cache.H):
         raise ValueError(f"acc: expected [{batch.B}, {cache.H}, n]")
-    _check(N.lib().fa_paged_weights(ref(tq), _dense(lse, torch.float32, "lse", (tq.T, tq.H)), ref(cache._c), ref(batch._c),
+    _check(N.lib().fa_paged_weights(ref(tq), _dense(lse, torch.float32, "lse", (tq.T, tq.H)), ref(cache.c()), ref(batch.c()),
                                     1 if causal else 0, float(softmax_scale), _dense(acc, torch.float32, "acc"),
                                     acc.shape[2], 1 if accumulate else 0, _here()), "fa_paged_weights")
     return acc
@@ -279,13 +307,14 @@ def paged_evict(cache: PagedCache, batch: PagedBatch, scores: torch.Tensor, budg
     int32 [B]; scores_out receives the kept tokens' scores, then zeros."""
     if scores.dim() != 3 or tuple(scores.shape[:2]) != (batch.B, cache.H):
         raise ValueError(f"scores: expected [{batch.B}, {cache.H}, n]")
-    if budget < 1:
-        raise ValueError("budget must be at least 1")
+    budget, sink, recent = _int32(budget, "budget"), _int32(sink, "sink"), _int32(recent, "recent")
+    if not 1 <= budget <= 2**30:
+        raise ValueError("budget must be at least 1 and at most 2^30")
     ps = _dense(scores, torch.float32, "scores")
     po = None if scores_out is None else _dense(scores_out, torch.float32, "scores_out", scores.shape)
     kept = scores.new_empty((batch.B, cache.H, budget), dtype=torch.int32)
     new = scores.new_empty((batch.B,), dtype=torch.int32)
-    _check(N.lib().fa_paged_evict(ctypes.byref(cache._c), ctypes.byref(batch._c), ps, scores.shape[2], int(budget),
-                                  int(sink), int(recent), kept.data_ptr(), new.data_ptr(), po, _here()),
+    _check(N.lib().fa_paged_evict(ctypes.byref(cache.c()), ctypes.byref(batch.c()), ps, scores.shape[2], budget, sink,
+                                  recent, kept.data_ptr(), new.data_ptr(), po, _here()),
            "fa_paged_evict")
     return kept, new

@@ -201,3 +201,17 @@ def test_binding_refuses_what_the_boundary_cannot_see():
         faq.empty_paged_cache(4, 2, 16, 64, "float", device="cpu")
     with pytest.raises(ValueError):
         faq.PagedBatch(torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+
+
+def test_sizes_of_weights_and_eviction(N):
+    """No new token with accumulate=0 is work (zeros are written), so its buffers are checked; a budget past
+    2^30 is refused; score rows of no token need no buffer (the refusal is then that of the kept list)."""
+    L, c = N.lib(), cache(N)
+    b = batch(N)
+    none = rows(N, T=0, H=8)
+    run = lambda acc=0x90000, stride=128, add=0: L.fa_paged_weights(by(none), None, by(c), by(b), 1, 0.0, acc, stride, add, None)
+    assert run(acc=None) == INVALID and run(acc=0x90002) == INVALID
+    assert run(acc=None, add=1) == OK
+    b = batch(N, cu=None)
+    assert L.fa_paged_evict(by(c), by(b), 0x90000, 128, 2 ** 30 + 1, 0, 0, 0xA0000, 0xB0000, None, None) == UNSUPPORTED
+    assert L.fa_paged_evict(by(c), by(b), None, 0, 8, 0, 0, None, 0xB0000, None, None) == INVALID

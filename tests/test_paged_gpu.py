@@ -591,3 +591,65 @@ def test_tensors_of_another_kind_are_refused(faq):
         need = faq.paged_attention_workspace_size(q, c, b)
         faq.paged_attention(q, c, b, workspace=torch.empty(need + 1, dtype=torch.uint8).cuda()[1:])
     assert e.value.status == 7
+
+
+def test_weights_of_no_new_token_are_zero(faq):
+    """A call whose batch holds no new token at all still sets the weights when it does not accumulate."""
+    for mode in ("int8_per_head", "fp8_per_token"):
+        table, pages = ref.make_table((40, 0, 129), 16, 5)
+        c = ref.make_cache(mode, "BNSD", pages, 2, 16, 64, 3)
+        gc = to_gpu(faq, c)
+        gb = faq.PagedBatch(table.cuda(), torch.tensor((40, 0, 129), dtype=torch.int32).cuda(),
+                            torch.zeros(4, dtype=torch.int32).cuda())
+        q, lse = torch.zeros(0, 4, 64, dtype=torch.bfloat16).cuda(), torch.zeros(0, 4).cuda()
+        for add in (True, False):
+            acc = torch.full((3, 2, 140), 5.0).cuda()
+            faq.paged_weights(q, lse, gc, gb, acc, accumulate=add)
+            faq.check_device_status()
+            want = torch.full((3, 2, 140), 5.0)
+            if not add:
+                want[0, :, :40], want[2, :, :129] = 0.0, 0.0
+            assert torch.equal(acc.cpu(), want)
+
+
+def test_empty_scores_of_empty_sequences(faq):
+    c = faq.empty_paged_cache(4, 2, 16, 64, "int8_per_token")
+    b = faq.PagedBatch(torch.zeros(3, 0, dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int32).cuda())
+    none = torch.zeros(3, 2, 0).cuda()
+    kept, new = faq.paged_evict(c, b, none, 4, scores_out=torch.zeros_like(none))
+    q, lse = torch.zeros(3, 4, 64, dtype=torch.bfloat16).cuda(), torch.zeros(3, 4).cuda()
+    out, z = faq.paged_attention(q, c, b, return_lse=True)
+    faq.paged_weights(q, z, c, b, none, accumulate=False)
+    faq.check_device_status()
+    assert (kept == -1).all() and (new == 0).all()
+    assert (out == 0).all() and torch.isneginf(z).all()
+
+
+def test_descriptors_stay_with_their_tensors_and_device(faq, monkeypatch):
+    import dataclasses
+
+    import quantized_attention_amax_b200.paged as paged
+    c = faq.empty_paged_cache(4, 2, 16, 64, "int8_per_token")
+    b = faq.PagedBatch(torch.zeros(1, 2, dtype=torch.int32).cuda(), torch.ones(1, dtype=torch.int32).cuda())
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16).cuda()
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        b.seq_lens = torch.zeros(1, dtype=torch.int32).cuda()
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        c.k_codes = c.v_codes
+    need = faq.paged_attention_workspace_size(q, c, b)
+    with pytest.raises(ValueError):
+        faq.paged_attention(q, c, b, workspace=torch.empty(need, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        faq.paged_attention(q, c, b, workspace=torch.empty(2 * need, dtype=torch.uint8).cuda()[::2])
+    scores = torch.zeros(1, 2, 32).cuda()
+    for kw in (dict(budget=2 ** 32 + 4), dict(budget=2 ** 30 + 1), dict(budget=8, sink=2 ** 32), dict(budget=8, recent=2 ** 32)):
+        with pytest.raises(ValueError):
+            faq.paged_evict(c, b, scores, **kw)
+    with pytest.raises(ValueError):
+        faq.PagedBatch(b.page_table, b.seq_lens, None, 2 ** 32)
+    # with another device current, no call takes them (the check comes before any launch)
+    there = torch.cuda.current_device() + 1
+    monkeypatch.setattr(paged, "_current_device", lambda: there)
+    for use in (c.c, b.c):
+        with pytest.raises(ValueError):
+            use()

@@ -17,6 +17,11 @@
 // the largest of them, whatever the scales' range: w_j = s_v(j) 2^(x_j - mv), mv the running maximum of
 // x + log2 s_v, and the sum of p is that of 2^(x_j - mv).
 // Work is shared out as paged_sched.cuh says: a causal block counts the key tiles it sees.
+// Measured: two chunks of up to 1500 tokens behind up to 32768, 32 / 8 heads of 128: int8 per head 1.60 ms (815 TFLOP/s,
+// 49 % of the library GEMM's rate), fp8 per head 1.66, fp8 per token 2.97 ms (440 TFLOP/s; 11.2 ms with warp-level MMAs).
+// Per head, a step of both tiles takes about 4000 cycles where the exponentials alone take 2048: the chain from one
+// product through a softmax to the next.  Per token the softmax is the longer side (3100 to 4500 cycles): both scales of
+// every key come from shared memory for every row, and their latency shows with two warps to a scheduler.
 #include "paged_sched.cuh"
 
 namespace faq {
@@ -105,13 +110,12 @@ struct Bool {
 struct Piece {
   int b, hk, q0, m, n;  // the sequence and kv head
   int row0;             // the block's first row
-  int t0, t1;
+  int t0, t1_last;      // (t1 << 1) + (no piece follows): one word, so that a reader that has t1 has the flag
   int kt[2];            // key tiles that the rows of tile A / B see
   int dual;             // both tiles hold the block's rows (at most 128), and share the key tiles out
   int whole;            // the piece is the whole item
   int slot;             // of its partial result
-  int last;             // no piece follows
-  int pad[2];
+  int pad[3];
 };
 constexpr int NPC = 4;  // pieces in the ring
 
@@ -144,10 +148,9 @@ __device__ __forceinline__ Piece make_piece(const AttnP& p, const Item& it, long
   }
   const long long item_end = it.first + it.nt, e = item_end < u1 ? item_end : u1;
   o.t0 = (int)(u - it.first);
-  o.t1 = max(o.t0, min((int)(e - it.first), max(o.kt[0], o.kt[1])));
+  o.t1_last = max(o.t0, min((int)(e - it.first), max(o.kt[0], o.kt[1]))) * 2 + (item_end >= u1);
   o.whole = u == it.first && item_end <= u1;
   o.slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
-  o.last = item_end >= u1;
   return o;
 }
 
@@ -227,7 +230,9 @@ __global__ void __launch_bounds__(CT, 1)
         if (k >= NPC && !(ok = wwait(C_PCE + k % NPC, k / NPC - 1, 240))) break;
         Piece pc = make_piece<PL>(p, it, u, u0, u1);
         u = it.first + it.nt;
-        if (!pc.last && !next_item<PL>(p, it)) pc.last = 1;  // cannot be while the lengths stay as they were counted
+        // (no next item cannot be while the lengths stay as they were counted)
+        if (!(pc.t1_last & 1) && !next_item<PL>(p, it)) pc.t1_last |= 1;
+        const int t1 = pc.t1_last >> 1;
         if (lane == 0) {
           pieces[k % NPC] = pc;
           mbar_arrive(&bar[C_PCF + k % NPC]);
@@ -236,14 +241,14 @@ __global__ void __launch_bounds__(CT, 1)
         auto page = [&](int t) {
           const int key = t * TN + (lane & 7) * 16;
           int pg = p.c.pages;
-          if (t < pc.t1 && key < pc.n) {
+          if (t < t1 && key < pc.n) {
             pg = page_of(p.bt, p.c, pc.b, key, p.status, 212);
             if (pg < 0) pg = p.c.pages;
           }
           return pg;
         };
-        int pages = pc.t0 < pc.t1 ? page(pc.t0) : 0;
-        for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+        int pages = pc.t0 < t1 ? page(pc.t0) : 0;
+        for (int t = pc.t0; t < t1 && ok; ++t) {
           const int next = page(t + 1);  // its latency passes while this tile's units wait
 #pragma unroll 1
           for (int q = 0; q < 2 * L::UT; ++q, ++g) {
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(CT, 1)
           }
           pages = next;
         }
-        if (pc.last) break;
+        if (pc.t1_last & 1) break;
       }
       if (*abort_flag)  // let the issued loads land before the CTA can leave
         for (int t = max(0, g - NU); t < g; ++t) mbar_drain(&bar[C_RF + t % NU], (t / NU) & 1);
@@ -274,16 +279,19 @@ __global__ void __launch_bounds__(CT, 1)
         const uint64_t dk = make_sdesc(smem_u32(smem + L::K), 16, 1024, kSwz128);
         const uint64_t dv = make_sdesc(smem_u32(smem + L::V), L::ATOM, 1024, kSwz128);
         const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
-        int base = 0;           // tiles of the pieces before this one
+        int base = 0, nq = 0;   // tiles of the pieces before this one, pieces with tiles
         int done[2] = {0, 0};   // tiles of A / B so far
         bool ok = true, more = true;
         for (int k = 0; ok && more; ++k) {
           if (!(ok = wait(C_PCF + k % NPC, k / NPC, 239))) break;
           const Piece& pc = pieces[k % NPC];
-          const int t0 = pc.t0, t1 = pc.t1, kt0 = pc.kt[0], kt1 = pc.kt[1], dual = pc.dual;
-          more = !pc.last;
-          mbar_arrive(&bar[C_PCE + k % NPC]);
-          if (!(ok = wait(C_Q, k, 241))) break;
+          const int t0 = pc.t0, t1 = pc.t1_last >> 1, kt0 = pc.kt[0], kt1 = pc.kt[1], dual = pc.dual;
+          more = !(pc.t1_last & 1);
+          if (t0 >= t1) {
+            mbar_arrive(&bar[C_PCE + k % NPC]);
+            continue;
+          }
+          if (!(ok = wait(C_Q, nq++, 241))) break;
           tc_fence_after();
           const int step = dual ? 2 : 1;
           auto has = [&](int x, int t) { return has_tile(t0, t1, x ? kt1 : kt0, dual, x, t); };
@@ -327,6 +335,7 @@ __global__ void __launch_bounds__(CT, 1)
             }
           }
           base += t1 - t0;
+          mbar_arrive(&bar[C_PCE + k % NPC]);
         }
         mma_commit(&bar[C_FIN]);
         mbar_drain(&bar[C_FIN], 0);
@@ -352,11 +361,9 @@ __global__ void __launch_bounds__(CT, 1)
     for (int k = 0; ok && more; ++k) {
       if (!(ok = wwait(C_PCF + k % NPC, k / NPC, 239))) break;
       const Piece& pc = pieces[k % NPC];
-      const int hk = pc.hk, b = pc.b, n = pc.n, t0 = pc.t0, t1 = pc.t1;
+      const int hk = pc.hk, b = pc.b, n = pc.n, t0 = pc.t0, t1 = pc.t1_last >> 1;
       const int lim_lo = p.causal ? n - pc.m : n - 1;
-      more = !pc.last;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[C_PCE + k % NPC]);
+      more = !(pc.t1_last & 1);
       float sk = 0.0f, sv = 0.0f;  // this thread's key of the coming tile
       int raw_page = -1;           // its page in the tile after that, as it lies in the table
       auto load_page = [&](int t) {
@@ -396,6 +403,7 @@ __global__ void __launch_bounds__(CT, 1)
           sc[2 * TN + ct] = f;
           const bool any_f = __any_sync(0xffffffffu, f != 1.0f);
           const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sv));
+          __syncwarp();
           if (lane == 0) {
             sc[3 * TN + (warp & 3)] = any_f ? 1.0f : 0.0f;
             sc[3 * TN + 4 + (warp & 3)] = __uint_as_float(top);
@@ -443,8 +451,6 @@ __global__ void __launch_bounds__(CT, 1)
           uint4 xs[NP];
 #pragma unroll
           for (int q = 0; q < NP; ++q) xs[q] = *reinterpret_cast<const uint4*>(raw + q * 2048);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[C_RE + sl]);
 #pragma unroll
           for (int q = 0; q < NP; ++q) {
             const uint32_t w[4] = {xs[q].x, xs[q].y, xs[q].z, xs[q].w};
@@ -468,6 +474,10 @@ __global__ void __launch_bounds__(CT, 1)
             *reinterpret_cast<uint4*>(tile + at0 + q * RPP * 128) = odd ? hi : lo;
             *reinterpret_cast<uint4*>(tile + at1 + q * RPP * 128) = odd ? lo : hi;
           }
+          // the slot is given back once its values have been used: an arrive behind loads that are still on their way lets
+          // the next unit land under them
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C_RE + sl]);
           if (u % UT == UT - 1) {
             fence_async_smem();
             __syncwarp();
@@ -476,6 +486,8 @@ __global__ void __launch_bounds__(CT, 1)
         }
       }
       base += t1 - t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C_PCE + k % NPC]);
     }
   } else {
     regs_inc<RS>();
@@ -486,18 +498,18 @@ __global__ void __launch_bounds__(CT, 1)
     const uint32_t tS = tbase + L::TS0 + x * 128;
     const uint32_t tO = tbase + (x ? L::TO1 : L::TO0);
     float2* ml = reinterpret_cast<float2*>(smem + L::ML);
-    int base = 0, n_done = 0, n_dual = 0;
+    int base = 0, n_done = 0, n_dual = 0, nq = 0;
     int done_b = 0;  // tile A's view of tile B's count (blocks of at most 128 rows)
     bool ok = true, more = true;
     for (int k = 0; ok && more; ++k) {
       if (!(ok = wwait(C_PCF + k % NPC, k / NPC, 239))) break;
       const Piece& pc = pieces[k % NPC];  // kept until the piece is done
-      const int t0 = pc.t0, t1 = pc.t1, kt = pc.kt[x], dual = pc.dual;
-      more = !pc.last;
-      int lim;
-      float f;
-      bool warp_live;
-      {
+      const int t0 = pc.t0, t1 = pc.t1_last >> 1, kt = pc.kt[x], dual = pc.dual;
+      more = !(pc.t1_last & 1);
+      int lim = -1;
+      float f = 0.0f;
+      bool warp_live = false;
+      if (t0 < t1) {  // (a piece without keys has no products, and is not waited for)
         // ---- this thread's Q row as fp16, scaled by a power of two
         const Seq s = {pc.q0, pc.m, pc.n};
         const int hk = pc.hk, r = pc.row0 + i + (dual ? 0 : x * BM), ii = r / p.G;
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(CT, 1)
         tc_fence_before();
         mbar_arrive(&bar[C_Q]);
         // both warpgroups: none runs a piece ahead of the other (the merge of the two goes through ml)
-        if (!(ok = wwait(C_Q, k, 254))) break;
+        if (!(ok = wwait(C_Q, nq++, 254))) break;
       }
       const int lim_lo = p.causal ? pc.n - pc.m + pc.row0 / p.G : pc.n - 1;  // every row of the block sees the keys up to here
       // factors of V: 2^(x - m_run + 7), times s_v in the per-token modes, whose m_run is that of x + log2 s_v;
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(CT, 1)
       tc_fence_after();
       float m_ref = m_run == -INFINITY ? -INFINITY : m_run - kShift;  // l and O are in units of 2^m_ref
       float wa = 1.0f, wb = 0.0f;
-      if (dual) {
+      if (dual && t0 < t1) {
         if (x == 1) {
           ml[i] = make_float2(m_ref, l_run);
           mbar_arrive(&bar[C_ML]);

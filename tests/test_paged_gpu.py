@@ -653,3 +653,46 @@ def test_descriptors_stay_with_their_tensors_and_device(faq, monkeypatch):
     for use in (c.c, b.c):
         with pytest.raises(ValueError):
             use()
+
+
+@pytest.mark.parametrize("mode", ["fp8_per_head", "int8_per_token"])
+def test_chunk_attention_repeats_bit_for_bit(faq, mode):
+    """Many blocks of few key tiles, whose conversion runs ahead of the products: each of 40 calls gives the same
+    bits.  V's element d is 1 for the tokens of the d-th 16, so that with equal weights (q = 0) a row's element d is the
+    share of them that it sees: a tile read late would show as a share that is off."""
+    n, H, D, page = 1500, 8, 128, 64
+    lens, qlens = (n, 1200), (n, 1100)
+    table, pages = ref.make_table(lens, page, 2)
+    c = ref.make_cache(mode, "BNSD", pages, H, page, D, 4, spread=0.5)
+    for x in ("kc", "vc"):
+        c[x].zero_()
+        for b, m in enumerate(lens):
+            for j in range(m):
+                c[x][int(table[b, j // page]), :, j % page, j // 16] = 0x38 if mode.startswith("fp8") else 1
+    c["ks"].fill_(1.0), c["vs"].fill_(1.0)
+    gc, gb = to_gpu(faq, c), batch_of(faq, table, lens, qlens)
+    q = torch.zeros(sum(qlens), 4 * H, D, dtype=torch.bfloat16).cuda()
+    first, lse = faq.paged_attention(q, gc, gb, return_lse=True)
+    i = torch.cat([torch.arange(b - a, b) + 1 for a, b in zip(qlens, lens)]).double()  # keys a row sees
+    d = torch.arange(D).double() * 16
+    want = ((i[:, None] - d).clamp(0, 16) / i[:, None])[:, None].expand(-1, 4 * H, D)
+    # fp16 shares are 2^7 exactly and sums of them exact in fp32: what rounds is the quotient, and bf16
+    assert_within(first, want, want * (2.0 ** -8 + 2.0 ** -21), "shares")
+    for _ in range(40):
+        out, z = faq.paged_attention(q, gc, gb, return_lse=True)
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16)) and torch.equal(z, lse)
+    faq.check_device_status()
+
+
+def test_chunks_over_empty_sequences(faq):
+    """Blocks that see no key at all, many in a row, among blocks that do: zeros and -inf, and the others right."""
+    lens, qlens = (0, 0, 0, 300, 0, 0, 0, 0, 0, 0, 20, 0), (40, 300, 33, 200, 64, 17, 90, 40, 129, 300, 20, 70)
+    table, pages = ref.make_table(lens, 16, 9)
+    c = ref.make_cache("int8_per_token", "BNSD", pages, 2, 16, 128, 21, spread=0.5)
+    q = bf16((sum(qlens), 4, 128), 22, 1.5)
+    for causal in (False, True):
+        want, lse, tol, ltol = ref.attend(q, c, table, lens, qlens, causal)
+        out, z = faq.paged_attention(q.cuda(), to_gpu(faq, c), batch_of(faq, table, lens, qlens), causal=causal, return_lse=True)
+        faq.check_device_status()
+        assert_within(out, want, tol, "out")
+        assert_within(z, lse, ltol, "lse")

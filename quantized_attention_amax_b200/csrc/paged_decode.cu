@@ -1,7 +1,8 @@
 // paged_decode.cu -- attention of at most 16 query rows per kv head (single tokens, drafts) over a paged
 // 8-bit cache, on the tensor cores' 8-bit kinds.
 //
-// The cache's bytes bound it (2 n Hkv D of them per sequence), so nothing but the tensor core touches the
+// The cache's bytes bound it (2 n Hkv D of them per sequence; with 16 rows the softmax threads do, which hold all of a
+// key's rows), so nothing but the tensor core touches the
 // codes: TMA brings 128-key tiles of K and V, page by page, into swizzled shared memory, and they are MMA
 // operands as they are.  The query rows and the probabilities enter as three 8-bit digits each
 // (paged_digits.cuh), three MMA columns per row:
@@ -16,6 +17,10 @@
 // (per-head modes: w = p, mv = m): w is at most 1 whatever the scales' range.  O is kept in registers, rescaled as
 // mv moves.  Two CTAs per SM cover each other's chains; K / V rings of three tiles keep about 100 KB per CTA
 // in flight.  Work is shared out as paged_sched.cuh says; a CTA's rings run on across its items.
+// Measured (combine included): 16 sequences of up to 32768 tokens, 32 / 8 heads of 128, int8 per head (760 MB): 126 to
+// 139 us, 5.5 to 6.0 TB/s, 83 to 92 % of the copy bandwidth (with warp-level 16-bit MMAs on converted codes: 221);
+// one of 131071, fp8 per token: 65 us (42 at the copy bandwidth; the runs' starts and the combine are the rest); one
+// of 1000: 12.4 us, the two launches and one chain.
 #include "paged_digits.cuh"
 #include "paged_sched.cuh"
 

@@ -14,6 +14,9 @@
 // The scores (once) and the kept rows (read and written once) bound it; slices are kept in shared
 // memory between the passes.  The cluster is as large as the GPU's SMs allow for the number of
 // (sequence, head) pairs, up to 8 CTAs.
+// Measured: 8 sequences of up to 32768 tokens, 8 heads of 128, cut to 4096 (fp8 per token): 91 us, of which the moved rows'
+// bytes are 22 at the copy bandwidth: the passes follow one another, each with a cluster barrier, and 64 clusters of two
+// leave 20 SMs idle.  One sequence of 2000 cut to 512: 28 us, the chain of passes and barriers alone.
 #include <cooperative_groups.h>
 
 #include "paged_common.cuh"

@@ -71,7 +71,7 @@ def _rows(t: torch.Tensor, what: str) -> N.FaRows:
     return N.FaRows(t.data_ptr(), T, H, D, st[0] if T > 1 else H * D)
 
 
-@dataclass(frozen=True, eq=False)
+@dataclass(frozen=True, eq=False, init=False)
 class PagedCache:
     """Pages of quantized K and V (fa_paged_cache): codes [pages, H, page_size, D] (layout "BNSD") or
     [pages, page_size, H, D] ("BSND"), int8 or E4M3 bytes (uint8); scales fp32 [H] in the per-head
@@ -84,26 +84,23 @@ class PagedCache:
     mode: str
     layout: str = "BNSD"
 
-    def __post_init__(self):
-        if self.layout not in LAYOUTS:
-            raise ValueError(f"layout must be BNSD or BSND, got {self.layout!r}")
-        if self.mode not in _CODES:
-            raise ValueError(f"a paged cache's mode is one of {sorted(_CODES)}, got {self.mode!r}")
-        s = self.k_codes.shape
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, mode, layout="BNSD"):
+        if layout not in LAYOUTS:
+            raise ValueError(f"layout must be BNSD or BSND, got {layout!r}")
+        if mode not in _CODES:
+            raise ValueError(f"a paged cache's mode is one of {sorted(_CODES)}, got {mode!r}")
+        s = k_codes.shape
         if len(s) != 4:
             raise ValueError("codes: expected 4 dimensions")
-        put = lambda name, value: object.__setattr__(self, name, value)
-        put("pages", s[0])
-        put("D", s[3])
-        put("H", s[1] if self.layout == "BNSD" else s[2])
-        put("page_size", s[2] if self.layout == "BNSD" else s[1])
-        sc = (self.H,) if self.mode in _PER_HEAD else (self.pages, self.H, self.page_size)
-        dt = _CODES[self.mode]
-        put("_c", N.FaPagedCache(_dense(self.k_codes, dt, "k_codes"), _dense(self.v_codes, dt, "v_codes", s),
-                                 _dense(self.k_scales, torch.float32, "k_scales", sc),
-                                 _dense(self.v_scales, torch.float32, "v_scales", sc), MODES[self.mode], self.pages,
-                                 self.H, self.page_size, self.D, LAYOUTS[self.layout]))
-        put("_device", _current_device())
+        pages, H, page_size, D = s if layout == "BNSD" else (s[0], s[2], s[1], s[3])
+        sc = (H,) if mode in _PER_HEAD else (pages, H, page_size)
+        dt = _CODES[mode]
+        c = N.FaPagedCache(_dense(k_codes, dt, "k_codes"), _dense(v_codes, dt, "v_codes", s),
+                           _dense(k_scales, torch.float32, "k_scales", sc), _dense(v_scales, torch.float32, "v_scales", sc),
+                           MODES[mode], pages, H, page_size, D, LAYOUTS[layout])
+        # (frozen: written past __setattr__, and in one go, since a serving loop may make one per call)
+        self.__dict__.update(k_codes=k_codes, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales, mode=mode,
+                             layout=layout, pages=pages, H=H, page_size=page_size, D=D, _c=c, _device=_current_device())
 
     def c(self) -> N.FaPagedCache:
         """The descriptor, for a call on the current device."""
@@ -112,7 +109,7 @@ class PagedCache:
         return self._c
 
 
-@dataclass(frozen=True, eq=False)
+@dataclass(frozen=True, eq=False, init=False)
 class PagedBatch:
     """The sequences of one call (fa_paged_batch): page_table int32 [B, max_pages]; seq_lens int32 [B],
     cached tokens with the new ones; cu_q int32 [B + 1], the new tokens' row offsets (None: one new
@@ -123,17 +120,15 @@ class PagedBatch:
     cu_q: Optional[torch.Tensor] = None
     max_q: int = 0
 
-    def __post_init__(self):
-        if self.page_table.dim() != 2:
+    def __init__(self, page_table, seq_lens, cu_q=None, max_q=0):
+        if page_table.dim() != 2:
             raise ValueError("page_table: expected [B, max_pages]")
-        B, wide = self.page_table.shape
-        put = lambda name, value: object.__setattr__(self, name, value)
-        put("B", B)
-        put("_c", N.FaPagedBatch(_dense(self.page_table, torch.int32, "page_table"),
-                                 _dense(self.seq_lens, torch.int32, "seq_lens", (B,)),
-                                 None if self.cu_q is None else _dense(self.cu_q, torch.int32, "cu_q", (B + 1,)), B, wide,
-                                 _int32(self.max_q, "max_q")))
-        put("_device", _current_device())
+        B, wide = page_table.shape
+        c = N.FaPagedBatch(_dense(page_table, torch.int32, "page_table"), _dense(seq_lens, torch.int32, "seq_lens", (B,)),
+                           None if cu_q is None else _dense(cu_q, torch.int32, "cu_q", (B + 1,)), B, wide,
+                           _int32(max_q, "max_q"))
+        self.__dict__.update(page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, max_q=max_q, B=B, _c=c,
+                             _device=_current_device())
 
     def c(self) -> N.FaPagedBatch:
         """The descriptor, for a call on the current device."""

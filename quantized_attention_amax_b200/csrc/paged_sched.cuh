@@ -267,14 +267,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
       for (int k = part; k < n; k += splits) {
         const float4 v = ml[k][r];
         const float4 x = *(reinterpret_cast<const float4*>(p.part_o + row_of(k0 + k, r) * D) + ch);
-        if (v.x > -INFINITY) l[y] += attn::ex2(v.x - mn) * v.y;
+        // maxima pass over NaN, so a piece whose scores are all NaN has m = -inf, as one without keys has: its sum
+        // tells them apart (NaN or 0) and enters as it is, and so do sums of p v (0, or NaN)
+        l[y] += v.x > -INFINITY ? attn::ex2(v.x - mn) * v.y : v.y;
         const float w = v.z > -INFINITY ? attn::ex2(v.z - mvn) : 0.0f;
-        if (w != 0.0f) {  // a piece without weight may hold anything
-          acc[y].x += w * x.x;
-          acc[y].y += w * x.y;
-          acc[y].z += w * x.z;
-          acc[y].w += w * x.w;
-        }
+        acc[y].x += w * x.x;
+        acc[y].y += w * x.y;
+        acc[y].z += w * x.z;
+        acc[y].w += w * x.w;
       }
     }
   }

@@ -443,8 +443,12 @@ FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_ro
  *   products as sums of three 8-bit terms (INT8: 24-bit integers of the row's
  *   range; E4M3: at least 12 bits); more rows: Q as fp16 times a power of two
  *   per row (bf16 values exact down to 2^-29 of the row's largest), the
- *   probabilities as fp16.  A NaN E4M3 code, or a scale that is NaN or
- *   infinite, makes the rows that see its token NaN and no others.
+ *   probabilities as fp16.
+ *   What is no number reaches the rows that see its token and no others,
+ *   wherever the token lies: a NaN E4M3 code of K, or a K scale that is NaN or
+ *   infinite, makes their output and LSE NaN; a V scale their output; a NaN
+ *   E4M3 code of V its element of their output.  A query row that holds a NaN
+ *   or an infinity is NaN where it sees a key.
  */
 FAQ_API fa_status fa_paged_attention(const fa_rows* q, const fa_paged_cache* cache, const fa_paged_batch* batch,
                                      int causal, float softmax_scale, void* out, float* lse, void* workspace,

@@ -18,7 +18,7 @@
 // x + log2 s_v, and the sum of p is that of 2^(x_j - mv).
 // Work is shared out as paged_sched.cuh says: a causal block counts the key tiles it sees.
 // Measured: two chunks of up to 1500 tokens behind up to 32768, 32 / 8 heads of 128: int8 per head 1.57 ms (829 TFLOP/s,
-// 50 % of the library GEMM's rate), fp8 per head 1.76, fp8 per token 3.04 ms (429 TFLOP/s; 11.2 ms with warp-level MMAs).
+// 50 % of the library GEMM's rate), fp8 per head 1.58, fp8 per token 3.06 ms (426 TFLOP/s; 11.2 ms with warp-level MMAs).
 // Per head, a step of both tiles takes about 4000 cycles where the exponentials alone take 2048: the chain from one
 // product through a softmax to the next.  Per token the softmax is the longer side (3100 to 4500 cycles): both scales of
 // every key come from shared memory for every row, and their latency shows with two warps to a scheduler.
@@ -55,7 +55,8 @@ struct CL {
   static constexpr uint32_t SCB = 3 * TN * 4 + 64;
   static constexpr uint32_t ML = SC + NSC * SCB;       // [128] (m, l) of tile B (blocks of at most 128 rows)
   static constexpr uint32_t PC = ML + BM * 8;          // NPC pieces
-  static constexpr uint32_t BAR = PC + 4 * 64;
+  static constexpr uint32_t NAN_KEY = PC + 4 * 64;     // NPC x ([128] per dim, [4]: of the V scales): the lowest key that is no number
+  static constexpr uint32_t BAR = NAN_KEY + 4 * 132 * 4;
   static constexpr int UR = 8192 / D;                  // keys of a load unit
   static constexpr int UT = TN / UR;                   // units of a tile of one operand
   static constexpr uint32_t UNIT = UR * D;             // raw codes: 8 KB
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(CT, 1)
   auto wait = [&](int which, int phase, int where) { return mbar_wait(&bar[which], phase & 1, abort_flag, p.status, where); };
   auto wwait = [&](int which, int phase, int where) { return __all_sync(0xffffffffu, wait(which, phase, where)); };
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::PC);
+  int* nan_keys = reinterpret_cast<int*>(smem + L::NAN_KEY);
 
   if (warp < 4) {
     regs_dec<R0>();
@@ -233,6 +235,9 @@ __global__ void __launch_bounds__(CT, 1)
         // (no next item cannot be while the lengths stay as they were counted)
         if (!(pc.t1_last & 1) && !next_item<PL>(p, it)) pc.t1_last |= 1;
         const int t1 = pc.t1_last >> 1;
+        if (FP8 || TOK)
+          for (int d = lane; d < 132; d += 32) nan_keys[(k % NPC) * 132 + d] = 0x7FFFFFFF;
+        __syncwarp();
         if (lane == 0) {
           pieces[k % NPC] = pc;
           mbar_arrive(&bar[C_PCF + k % NPC]);
@@ -363,6 +368,7 @@ __global__ void __launch_bounds__(CT, 1)
       const Piece& pc = pieces[k % NPC];
       const int hk = pc.hk, b = pc.b, n = pc.n, t0 = pc.t0, t1 = pc.t1_last >> 1;
       const int lim_lo = p.causal ? n - pc.m : n - 1;
+      int* nan_key = nan_keys + (k % NPC) * 132;
       more = !(pc.t1_last & 1);
       float sk = 0.0f, sv = 0.0f;  // this thread's key of the coming tile
       int raw_page = -1;           // its page in the tile after that, as it lies in the table
@@ -386,11 +392,11 @@ __global__ void __launch_bounds__(CT, 1)
         const int j = base + t - t0, st = j % NSG, ss = j % NSC;
         float* sc = reinterpret_cast<float*>(smem + L::SC + ss * L::SCB);
         if (TOK) {
-          // s_k, s_v and the factor of the V codes (1 but for tiny scales).  A NaN or infinite s_v is given to
-          // the rows that see the key by s_k.
+          // s_k, s_v and the factor of the V codes (1 but for tiny scales).  The rows that see a key whose s_v is NaN or
+          // infinite get their NaN when they are written.
           float f = 1.0f;
           if (!(fabsf(sv) < INFINITY)) {
-            sk = __uint_as_float(0x7FC00000u);
+            atomicMin(nan_key + 128, t * TN + ct);
             f = 0.0f;
             sv = kMinScale;
           } else if (sv < kMinScale) {
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(CT, 1)
             sv = kMinScale;
           }
           if (j >= NSC && !(ok = wwait(C_SCE + ss, j / NSC - 1, 245))) break;
-          sc[ct] = sk;
+          sc[ct] = finite_or_nan(sk);
           sc[TN + ct] = sv;
           sc[2 * TN + ct] = f;
           const bool any_f = __any_sync(0xffffffffu, f != 1.0f);
@@ -412,10 +418,8 @@ __global__ void __launch_bounds__(CT, 1)
           load_scales(t + 1, raw_page);
           raw_page = load_page(t + 2);
         }
-        // In a tile that not every row sees whole, V rows past the end are cleared, and rows with E4M3 NaN
-        // codes too (0 times NaN is NaN), whose key's K row becomes NaN for the rows that see it.
+        // in a tile that not every row sees whole, V rows past the end are cleared, and NaN codes
         const bool edge = FP8 && t * TN + TN - 1 > lim_lo;
-        uint32_t clear = 0;  // bit NP u + q: pass q of unit u's rows
 #pragma unroll 1
         for (int u = 0; u < 2 * UT; ++u, ++g) {
           const int sl = g % NU;
@@ -423,23 +427,24 @@ __global__ void __launch_bounds__(CT, 1)
           if (u == 0 && j >= NSG && !(ok = wwait(C_KE + st, j / NSG - 1, 246))) break;
           if (u == UT && j >= NSG && !(ok = wwait(C_VE + st, j / NSG - 1, 247))) break;
           if (u == UT && TOK && !(ok = wwait(C_SCF + ss, j / NSC, 255))) break;  // the other warps' factors
-          uint32_t k_nan = 0;
-          if (edge && u < UT) {
-            static_assert(NU > UT, "unit u + UT is in the ring while unit u is converted");
-            if (!(ok = wwait(C_RF + (g + UT) % NU, (g + UT) / NU, 236))) break;
-#pragma unroll
+          if (FP8 && edge && u >= UT) {  // this thread's chunks, in the staging slot
+#pragma unroll 1
             for (int q = 0; q < NP; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(smem + L::RAW + ((g + UT) % NU) * L::UNIT + q * 2048 + ct * 16);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              bool nan = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) nan = nan || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-              const unsigned hit = __ballot_sync(0xffffffffu, nan);
-              const bool row_nan = (hit & (((1u << LPR) - 1u) << (lane / LPR * LPR))) != 0;
-              const bool past = t * TN + u * UR + r0 + q * RPP >= n;
-              if (row_nan || past) clear |= 1u << (NP * u + q);
-              if (row_nan && !past) k_nan |= 1u << q;
+              const int key = t * TN + (u - UT) * UR + r0 + q * RPP;
+              uint32_t* at = reinterpret_cast<uint32_t*>(smem + L::RAW + sl * L::UNIT + ct * 16 + q * 2048);
+              const uint4 x = *reinterpret_cast<const uint4*>(at);
+              if (key >= n) {
+                *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+              } else if (e4m3_nans(x.x) | e4m3_nans(x.y) | e4m3_nans(x.z) | e4m3_nans(x.w)) {
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t nans = e4m3_nans(at[e]);
+                  note_nans(nans, 16 * c + 4 * e, key, nan_key);
+                  at[e] &= ~((nans >> 7) * 0xFFu);
+                }
+              }
             }
+            fence_async_smem();  // the slot's next bytes come by TMA
           }
           uint8_t* tile = smem + (u < UT ? L::K : L::V) + st * L::TILE + (u % UT) * UR * 128;
           const uint8_t* raw = smem + L::RAW + sl * L::UNIT + ct * 16;
@@ -457,11 +462,6 @@ __global__ void __launch_bounds__(CT, 1)
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) codes4_to_h2<FP8>(w[e], h[2 * e], h[2 * e + 1]);
-            if (FP8 && edge) {
-              const bool zero = u >= UT && ((clear >> (NP * (u - UT) + q)) & 1u), nan = (k_nan >> q) & 1u;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) h[e] = zero ? 0u : nan ? 0x7FFF7FFFu : h[e];
-            }
             if (scaled) {
               const __half2 f2 = __float2half2_rn(sc[2 * TN + (u - UT) * UR + r0 + q * RPP]);
 #pragma unroll
@@ -527,8 +527,11 @@ __global__ void __launch_bounds__(CT, 1)
           for (int e = 0; e < 4; ++e)
             m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
         }
+        const float head_scale = TOK ? 1.0f : __ldg(p.c.ks + hk);
         float inv;
-        const float sc = pow2_to_fp16(m, inv);
+        float sc = pow2_to_fp16(m, inv);
+        // a query or K scale that is no number: NaN in the row's operand, so that the keys it does not see stay masked
+        if (!(m < INFINITY) || !(fabsf(head_scale) < INFINITY)) sc = __uint_as_float(0x7FC00000u);
         uint8_t* qt = smem + L::Q + x * L::TILE;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
@@ -542,8 +545,8 @@ __global__ void __launch_bounds__(CT, 1)
           }
           *reinterpret_cast<uint4*>(qt + (c >> 3) * L::ATOM + swz128_offset(i, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        f = p.scale_log2 * inv * (TOK ? 1.0f : __ldg(p.c.ks + hk));
-        if (f == 0.0f) f = 1e-37f;  // a zero K scale: scores vanish, and hidden keys stay at -inf
+        f = p.scale_log2 * inv * head_scale;
+        if (f == 0.0f || sc != sc) f = 1e-37f;  // a zero K scale: scores vanish, and hidden keys stay at -inf
         fence_async_smem();
         tc_fence_before();
         mbar_arrive(&bar[C_Q]);
@@ -758,6 +761,8 @@ __global__ void __launch_bounds__(CT, 1)
         const long long slot_row = (long long)pc.slot * PL::RB + (r - pc.row0);
         const long long out_row = (long long)(pc.q0 + ii) * p.Hq + hk * p.G + r - ii * p.G;
         const float fac = whole ? row_factor(p, hk, l_run, m_ref, m_ref) : 1.0f;
+        const int* nan_key = nan_keys + (k % NPC) * 132;
+        const bool all_nan = TOK && nan_key[128] <= lim;
         if (live) {
           if (whole) {
             if (p.lse) p.lse[out_row] = row_lse(l_run, m_ref);
@@ -774,9 +779,10 @@ __global__ void __launch_bounds__(CT, 1)
           float y[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            y[k] = any && wa != 0.0f ? __uint_as_float(o[k]) * wa : 0.0f;
-            if (any_b && wb != 0.0f) y[k] += __uint_as_float(ob[k]) * wb;
+            y[k] = any ? __uint_as_float(o[k]) * wa : 0.0f;
+            if (any_b) y[k] += __uint_as_float(ob[k]) * wb;
             y[k] *= fac;
+            if (all_nan || (FP8 && nan_key[c * 16 + k] <= lim)) y[k] = __uint_as_float(0x7FC00000u);
           }
           if (live && whole) {
             uint32_t h[8];

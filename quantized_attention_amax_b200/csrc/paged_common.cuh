@@ -76,6 +76,19 @@ __device__ __forceinline__ int page_of(const Batch& bt, const Cache& c, int b, i
   return pg;
 }
 
+// A scale as the kernels use it: one that is NaN or infinite makes what it scales NaN.
+__device__ __forceinline__ float finite_or_nan(float s) { return fabsf(s) < INFINITY ? s : __uint_as_float(0x7FC00000u); }
+
+// The E4M3 NaN codes (0x7F and 0xFF) of a word's four: 0x80 in their bytes.
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Where V is no number: in a tile that some rows do not see whole, NaN codes would reach rows that do not see them (0
+// times NaN is NaN), so they are cleared, and the lowest key whose element d was one is kept for d here; the
+// rows that see that key get their NaN when they are written.
+__device__ __forceinline__ void note_nans(uint32_t nans, int d, int key, int* nan_key) {
+  for (; nans; nans &= nans - 1) atomicMin(nan_key + d + ((__ffs(nans) - 1) >> 3), key);
+}
+
 // Four codes of one word -> two fp16 pairs (bytes 0, 1 and 2, 3), exactly.
 template <bool FP8>
 __device__ __forceinline__ void codes4_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {

@@ -48,7 +48,8 @@ struct DL {
   static constexpr uint32_t RED = P + NP * N * 128;         // 2 x [4 warps][2 R] maxima
   static constexpr uint32_t SUM = RED + 2 * 4 * 2 * R * 4;  // [4 warps][R] sums
   static constexpr uint32_t ROW = SUM + 4 * R * 4;          // [R] factors, [R] limits
-  static constexpr uint32_t BAR = (ROW + 2 * R * 4 + 15) & ~15u;
+  static constexpr uint32_t NAN_KEY = ROW + 2 * R * 4;      // per dim (D = 64: of each half), and of each warp's V scales: the lowest key that is no number
+  static constexpr uint32_t BAR = (NAN_KEY + 132 * 4 + 15) & ~15u;
   static constexpr uint32_t TOTAL = BAR + 256;
   static constexpr uint32_t ALLOC = TOTAL + 1024;
   static constexpr uint32_t TO = NS * N;                    // TMEM: S^T buffers, then two of O^T
@@ -82,6 +83,29 @@ __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Row i of a swizzled V tile: all of it past the sequence's end, else its E4M3 NaN codes, cleared, and these noted for their
+// dims.  A call: its loops inlined cost the tiles that never come here 20 % (137 -> 165 us for 16 sequences of up to 32768
+// tokens, fp8 per token).
+template <int D>
+__device__ __noinline__ void clear_nans(uint8_t* tile, int i, bool past, int key, int* nan_key) {
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t* at = reinterpret_cast<uint32_t*>(tile + (D == 128 ? swz128_offset(i, c) : swz64_offset(i, c)));
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (past) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+    } else if (e4m3_nans(w[0]) | e4m3_nans(w[1]) | e4m3_nans(w[2]) | e4m3_nans(w[3])) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t nans = e4m3_nans(w[e]);
+        note_nans(nans, (D == 128 ? 0 : i & 64) + 16 * c + 4 * e, key, nan_key);
+        at[e] = w[e] & ~((nans >> 7) * 0xFFu);
+      }
+    }
+  }
 }
 
 // The CTA's run of units, piece by piece: an item's tiles [t0, t1).
@@ -271,6 +295,7 @@ __global__ void __launch_bounds__(DT, 2)
     float* halves = reinterpret_cast<float*>(smem + L::P);  // at a piece's end, when no P is in use
     float* rowf = reinterpret_cast<float*>(smem + L::ROW);
     int* rowl = reinterpret_cast<int*>(smem + L::ROW) + R;
+    int* nan_key = reinterpret_cast<int*>(smem + L::NAN_KEY);
     auto wait = [&](int which, int phase, int where) {
       return __all_sync(0xffffffffu, mbar_wait(&bar[which], phase & 1, abort_flag, p.status, where));
     };
@@ -327,10 +352,11 @@ __global__ void __launch_bounds__(DT, 2)
             *reinterpret_cast<uint4*>(smem + L::Q + swz(k * R + r, c)) =
                 make_uint4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
           if (c == 0) {
-            rowf[r] = p.scale_log2 * inv * (TOK ? 1.0f : __ldg(p.c.ks + hk));
+            rowf[r] = p.scale_log2 * inv * (TOK ? 1.0f : finite_or_nan(__ldg(p.c.ks + hk)));
             rowl[r] = row_limit(p, s, r);
           }
         }
+        if (FP8) nan_key[i] = 0x7FFFFFFF;
         fence_async_smem();
         mbar_arrive(&bar[B_Q]);
         ok = wait(B_Q, piece, 221);
@@ -341,6 +367,7 @@ __global__ void __launch_bounds__(DT, 2)
       const int lim_lo = p.causal ? s.n - s.m : s.n - 1;  // every row sees the keys up to here
       // per-token scales of this thread's key, one tile ahead; its page two tiles ahead
       float sk = 0.0f, sv = 0.0f, sk_n = 0.0f, sv_n = 0.0f;
+      int bad_key = 0x7FFFFFFF;  // this thread's lowest key whose V scale is no number
       int pg_n = -1;
       auto load_page = [&](int t) {
         const int key = t * TK + i;
@@ -367,25 +394,10 @@ __global__ void __launch_bounds__(DT, 2)
             pg_n = load_page(t + 2);
           }
         }
-        bool v_bad = TOK && !(fabsf(sv) < INFINITY);  // a NaN or infinite V scale: rows that see the key are NaN
         if (FP8 && masked) {
-          // V rows that not every row sees must be finite, since 0 times NaN is NaN: rows past the end
-          // are cleared, a row with NaN codes too, and its NaN is given to the rows that see it
+          // V codes that not every row sees must be finite: rows past the end are cleared, and NaN codes
           if (!(ok = wait(B_VF + j % NST, j / NST, 222))) break;
-          uint4* row = reinterpret_cast<uint4*>(smem + L::V + (j % NST) * TILE + i * HD);
-          bool nan = false;
-#pragma unroll
-          for (int c = 0; c < HD / 16; ++c) {
-            const uint4 x = row[c];
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) nan = nan || (((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-          }
-          if (key >= s.n || nan) {
-#pragma unroll
-            for (int c = 0; c < HD / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
-          }
-          v_bad = v_bad || (nan && key < s.n);
+          clear_nans<HD>(smem + L::V + (j % NST) * TILE, i, key >= s.n, key, nan_key);
         }
         if (!(ok = wait(B_SF + sb, j / NS, 223))) break;
         tc_fence_after();
@@ -397,13 +409,15 @@ __global__ void __launch_bounds__(DT, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[B_SE + sb]);
         // ---- scores and the rows' maxima
+        const bool v_bad = TOK && !(fabsf(sv) < INFINITY);  // a NaN or infinite V scale: rows that see the key are NaN
+        bad_key = min(bad_key, v_bad ? key : 0x7FFFFFFF);
+        if (TOK) sk = finite_or_nan(sk);
         float x[R];
         const float lsv = TOK ? log2f(v_bad ? 0.0f : sv) : 0.0f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           x[r] = join_digits<FP8>(a[r], a[R + r], a[2 * R + r]) * f[r];
           if (TOK) x[r] *= sk;
-          if (v_bad) x[r] = __uint_as_float(0x7FC00000u);
           if (masked && key > rowl[r]) x[r] = -INFINITY;
           const float mx = warp_max(x[r]);
           const float mt = TOK ? warp_max(x[r] + lsv) : mx;
@@ -436,12 +450,11 @@ __global__ void __launch_bounds__(DT, 2)
             const float vn = fmaxf(mv_run[r], fmaxf(fmaxf(rv[0], rv[2 * R]), fmaxf(rv[4 * R], rv[6 * R])));
             al_new[r] = vn == mv_run[r] ? 1.0f : attn::ex2(mv_run[r] - vn);
             mv_run[r] = vn;
-            // not p s_v: p may vanish where s_v is large; a masked or bad key has weight 0 here
+            // not p s_v: p may vanish where s_v is large; a masked key, or one whose s_v is no number, has weight 0 here
             w = vn == -INFINITY || !(x[r] > -INFINITY) || v_bad ? 0.0f : attn::ex2(x[r] + lsv - vn);
           } else {
             al_new[r] = mn == mv_run[r] ? 1.0f : attn::ex2(mv_run[r] - base);
             mv_run[r] = mn;
-            if (v_bad) w = 0.0f;
           }
           uint32_t d[3];
           p_digits<FP8>(w, d);
@@ -483,9 +496,17 @@ __global__ void __launch_bounds__(DT, 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[B_OE + jb]);
+        int lim[R];
+        if (TOK) {
+          bad_key = __reduce_min_sync(0xffffffffu, bad_key);
+          if (lane == 0) nan_key[128 + wg] = bad_key;
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           o[r] = o[r] * al_o[r] + join_digits<FP8>(a[r], a[R + r], a[2 * R + r]);
+          // every key's thread has noted its NaN codes before the last tile's maxima
+          if (FP8 && nan_key[i] <= rowl[r]) o[r] = __uint_as_float(0x7FC00000u);
+          if (TOK) lim[r] = rowl[r];  // (read before B_SUM: the next piece's limits come after it)
           float l = l_run[r];
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
@@ -495,8 +516,10 @@ __global__ void __launch_bounds__(DT, 2)
         mbar_arrive(&bar[B_SUM]);
         if (!(ok = wait(B_SUM, piece, 228))) break;
         ++piece;
+        if (TOK) bad_key = min(min(nan_key[128], nan_key[129]), min(nan_key[130], nan_key[131]));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+          if (TOK && bad_key <= lim[r]) o[r] = __uint_as_float(0x7FC00000u);
           if (HD == 64 && !half) o[r] += halves[r * 64 + i];
           l_run[r] = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
         }

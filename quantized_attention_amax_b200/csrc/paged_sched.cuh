@@ -186,7 +186,7 @@ __device__ __forceinline__ int row_limit(const AttnP& p, const Seq& s, int r) {
 // One row's result from its merged sums: bf16 values a f, and the LSE.
 __device__ __forceinline__ float row_factor(const AttnP& p, int hk, float l, float m, float mv) {
   if (!(l > 0.0f) && l == l) return 0.0f;  // no key seen
-  return (p.c.per_token ? attn::ex2(mv - m) : __ldg(p.c.vs + hk)) / l;
+  return (p.c.per_token ? attn::ex2(mv - m) : finite_or_nan(__ldg(p.c.vs + hk))) / l;
 }
 __device__ __forceinline__ float row_lse(float l, float m) { return (m + log2f(l)) * 0.69314718055994530942f; }
 

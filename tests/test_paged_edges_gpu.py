@@ -102,3 +102,89 @@ def test_a_nan_head_scale_over_a_cut_history(faq, rows, mode):
     bad = torch.zeros(rows, 4, dtype=torch.bool)
     bad[:, 2:] = True
     expect_rows(attend(faq, q, c, table, lens, qlens), want, bad)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("mode", ["fp8_per_head", "fp8_per_token"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [300, 5000])
+def test_a_nan_value_code_reaches_its_element(faq, rows, mode, D, n):
+    """A NaN E4M3 code of V makes that element of the rows that see its token NaN, wherever the token lies: in a tile
+    that every row sees whole, or in one that some do not.  The rows' other elements, their LSE and the other rows
+    are as without it."""
+    lens, qlens = (n, 40), (rows, 1)
+    table, pages = ref.make_table(lens, 16, 2)
+    c = ref.make_cache(mode, "BNSD", pages, 1, 16, D, 3, spread=0.5)
+    q = bf16((rows + 1, 2, D), 4)
+    out, lse, tol, ltol = ref.attend(q, c, table, lens, qlens, True)
+    nan = torch.zeros(rows + 1, 2, D, dtype=torch.bool)
+    i = torch.arange(rows)
+    for j, d in ((5, 3), (n - 1, 0), (n - 1, 40), (n - rows, D - 1), (n - 1 - rows // 2, 17), (n - 1, 17), (n // 2, 33)):
+        pg, o = slot(table, 16, j)
+        put(c, "v", pg, 0, o, (d, 0x7F if j & 1 else 0xFF))
+        nan[:rows, :, d] |= (n - rows + i >= j)[:, None]
+    pg, o = slot(table, 16, 39, 1)
+    put(c, "v", pg, 0, o, (11, 0x7F))
+    nan[rows, :, 11] = True
+    got, z = attend(faq, q, c, table, lens, qlens)
+    assert torch.equal(torch.isnan(got), nan)
+    assert_within(got[~nan], out[~nan], tol[~nan], "out")
+    assert_within(z, lse, ltol, "lse")
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("mode", ["int8_per_token", "fp8_per_token"])
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("n", [129, 2000])
+def test_a_value_scale_that_is_no_number(faq, rows, mode, value, n):
+    """The rows that see the token are NaN; their LSE, which V has no part in, is as without it."""
+    for j in (n - 1, n - 1 - rows // 2, 3):
+        lens, qlens = (n, 20), (rows, 2)
+        table, pages = ref.make_table(lens, 16, 2)
+        c = ref.make_cache(mode, "BSND", pages, 1, 16, 128, 3, spread=0.5)
+        q = bf16((rows + 2, 2, 128), 4)
+        out, lse, tol, ltol = ref.attend(q, c, table, lens, qlens, True)
+        pg, o = slot(table, 16, j)
+        c["vs"][pg, 0, o] = value
+        nan = torch.zeros(rows + 2, 2, dtype=torch.bool)
+        nan[:rows] = (n - rows + torch.arange(rows) >= j)[:, None]
+        got, z = attend(faq, q, c, table, lens, qlens)
+        assert torch.isnan(got[nan]).all()
+        assert_within(got[~nan], out[~nan], tol[~nan], "out")
+        assert_within(z, lse, ltol, "lse")
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("mode", ref.MODES)
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_scales_of_a_head_that_are_no_numbers(faq, rows, mode, value):
+    """K scales: the rows that see such a token are NaN, output and LSE, whatever its scores' signs.  V scales: the output.
+    Rows that see no key stay zero and -inf."""
+    lens, qlens = (2000, 1, 0), (rows, rows + 2, rows)
+    table, pages = ref.make_table(lens, 16, 2)
+    T = sum(qlens)
+    q = bf16((T, 4, 64), 4)
+    q[:, 2:] = q[:, 2:].abs()
+    see = torch.zeros(T, 4, dtype=torch.bool)
+    see[:rows] = True
+    see[2 * rows + 1] = True  # the second sequence's one token is seen by its last row
+    for which in ("ks", "vs"):
+        c = ref.make_cache(mode, "BNSD", pages, 2, 16, 64, 3, spread=0.5)
+        if which == "ks":  # every score of head 1's rows below zero
+            k = c["kc"][:, 1]
+            c["kc"][:, 1] = k | 0x80 if mode.startswith("fp8") else -(k.abs().clamp(1, 127))
+        out, lse, tol, ltol = ref.attend(q, c, table, lens, qlens, True)
+        if mode in ref.PER_HEAD:
+            c[which][1] = value
+        else:
+            c[which][:, 1] = value
+        got, z = attend(faq, q, c, table, lens, qlens)
+        hit = see.clone()
+        hit[:, :2] = False
+        assert torch.isnan(got[hit]).all()
+        assert_within(got[~hit], out[~hit], tol[~hit], "out")
+        if which == "ks":
+            assert torch.isnan(z[hit]).all()
+            assert_within(z[~hit], lse[~hit], ltol[~hit], "lse")
+        else:
+            assert_within(z, lse, ltol, "lse")

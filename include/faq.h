@@ -439,11 +439,17 @@ FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_ro
  *   calls that can overlap (two streams) need one each.
  *   out must not overlap q.
  *   Scores, maxima, sums and accumulators are fp32.  Sequences of at most 16
- *   query rows per kv head (m_b * Hq / Hkv): Q and the probabilities enter the
- *   products as sums of three 8-bit terms (INT8: 24-bit integers of the row's
- *   range; E4M3: at least 12 bits); more rows: Q as fp16 times a power of two
- *   per row (bf16 values exact down to 2^-29 of the row's largest), the
- *   probabilities as fp16.
+ *   query rows per kv head (m_b * Hq / Hkv): Q and the probabilities (times
+ *   s_v, per token) enter the products as sums of three 8-bit terms.  INT8: Q
+ *   as 22-bit integers of the row's range, a probability as a 24-bit one of the
+ *   largest of its 128 keys (cache indices 128 t .. 128 t + 127); E4M3: with at
+ *   least 12 bits each, but no finer than 2^-25 of the row's largest |q|, or
+ *   of the largest probability of the 128 keys.  More rows: Q as fp16
+ *   times a power of two per row (bf16 values exact down to 2^-29 of the row's
+ *   largest), the probabilities as fp16: 11 bits, and below 2^-21 of the row's
+ *   largest a half step of 2^-32 of it.  So n cached keys under 2^-32 of one
+ *   that outweighs them are lost from the output (n 2^-32 of its weight at
+ *   most), where the LSE still counts them.
  *   What is no number reaches the rows that see its token and no others,
  *   wherever the token lies: a NaN E4M3 code of K, or a K scale that is NaN or
  *   infinite, makes their output and LSE NaN; a V scale their output; a NaN

@@ -13,14 +13,17 @@
 // pair a half with itself count.
 // A softmax thread owns a key of S^T and a dim of O^T (D = 64: of one half's).  Per tile: join the digits' sums into scores, the rows'
 // maxima over the 128 keys (warp reductions, then the four warps through shared memory), p = 2^(x - m) into the row
-// sums, and the digits of w = p s_v 2^(m - mv) for the second product, mv the running maximum of x + log2 s_v
-// (per-head modes: w = p, mv = m): w is at most 1 whatever the scales' range.  O is kept in registers, rescaled as
-// mv moves.  Two CTAs per SM cover each other's chains; K / V rings of three tiles keep about 100 KB per CTA
+// sums, and the digits of w = s_v 2^(x - u) for the second product (per-head modes: w = p, without s_v), 2^u the tile's
+// own largest weight brought up to a power of two: w is at most 1 whatever the scales' range, and the digits'
+// fixed step stays small beside a tile's weights, however far these lie below the row's largest (a long history's many
+// small weights would otherwise count in the row sum alone).  O is kept in registers, rescaled by whole powers of two
+// from tile to tile.  Two CTAs per SM cover each other's chains; K / V rings of three tiles keep about 100 KB per CTA
 // in flight.  Work is shared out as paged_sched.cuh says; a CTA's rings run on across its items.
-// Measured (combine included): 16 sequences of up to 32768 tokens, 32 / 8 heads of 128, int8 per head (760 MB): 126 to
-// 139 us, 5.5 to 6.0 TB/s, 83 to 92 % of the copy bandwidth (with warp-level 16-bit MMAs on converted codes: 221);
-// one of 131071, fp8 per token: 65 us (42 at the copy bandwidth; the runs' starts and the combine are the rest); one
-// of 1000: 12.4 us, the two launches and one chain.
+// Measured (combine included): 16 sequences of up to 32768 tokens, 32 / 8 heads of 128, int8 per head (760 MB): 127 to
+// 130 us, 5.8 to 6.0 TB/s, 89 to 91 % of the copy bandwidth (with warp-level 16-bit MMAs on converted codes: 221), fp8 per token
+// 136; one of 131071, fp8 per token: 62 us (42 at the copy bandwidth; the runs' starts and the combine are the rest); one
+// of 1000: 12.6 us, the two launches and one chain; four tokens to each of 8 sequences of 32768: 138 us int8 per head, 183 fp8 per
+// token (182 and 350 when every thread kept every row's units in registers, which spilled).
 #include "paged_digits.cuh"
 #include "paged_sched.cuh"
 
@@ -31,6 +34,9 @@ using namespace paged;
 constexpr int TK = 128;     // keys per tile
 constexpr int NST = 3;      // K / V stages
 constexpr int DT = 192;     // warp 0 loads, warp 1 MMAs, warps 2-5 softmax
+// How far (powers of two) a tile's unit may lie below the largest: fp32 holds O in the lower one, and what 2^24 below it is
+// lost weighs 2^-84 of the largest weight.
+constexpr float kFall = 60.0f;
 
 using DPL = Plan<TK, 16, 1, 16>;
 
@@ -49,7 +55,8 @@ struct DL {
   static constexpr uint32_t SUM = RED + 2 * 4 * 2 * R * 4;  // [4 warps][R] sums
   static constexpr uint32_t ROW = SUM + 4 * R * 4;          // [R] factors, [R] limits
   static constexpr uint32_t NAN_KEY = ROW + 2 * R * 4;      // per dim (D = 64: of each half), and of each warp's V scales: the lowest key that is no number
-  static constexpr uint32_t BAR = (NAN_KEY + 132 * 4 + 15) & ~15u;
+  static constexpr uint32_t UNIT = NAN_KEY + 132 * 4;       // [4 warps][R] the tile's units, then 2 x [4][R] what O's changes by
+  static constexpr uint32_t BAR = UNIT + 4 * R * 16 + 2 * 4 * R * 4;
   static constexpr uint32_t TOTAL = BAR + 256;
   static constexpr uint32_t ALLOC = TOTAL + 1024;
   static constexpr uint32_t TO = NS * N;                    // TMEM: S^T buffers, then two of O^T
@@ -132,6 +139,7 @@ __global__ void __launch_bounds__(DT, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnP p) {
   using L = DL<HD, R>;
   constexpr int N = L::N, NO = L::NO, NS = L::NS;
+  constexpr int JOBS = TOK ? 2 * R : R;  // a tile's maxima: of x, and (per-token modes) of x + log2 s_v
   constexpr uint32_t TILE = L::TILE, SW = HD == 128 ? kSwz128 : kSwz64, SBO = 8 * HD;
   auto swz = [](uint32_t row, uint32_t chunk) { return HD == 128 ? swz128_offset(row, chunk) : swz64_offset(row, chunk); };
   extern __shared__ uint8_t smem_raw[];
@@ -296,6 +304,8 @@ __global__ void __launch_bounds__(DT, 2)
     float* rowf = reinterpret_cast<float*>(smem + L::ROW);
     int* rowl = reinterpret_cast<int*>(smem + L::ROW) + R;
     int* nan_key = reinterpret_cast<int*>(smem + L::NAN_KEY);
+    float4* units = reinterpret_cast<float4*>(smem + L::UNIT);
+    float* alb = reinterpret_cast<float*>(units + 4 * R);
     auto wait = [&](int which, int phase, int where) {
       return __all_sync(0xffffffffu, mbar_wait(&bar[which], phase & 1, abort_flag, p.status, where));
     };
@@ -304,13 +314,13 @@ __global__ void __launch_bounds__(DT, 2)
     do {
       const Seq s = run.it.s;
       const int hk = run.it.hk, b = run.it.b, rows = s.m * p.G;
-      float m_run[R], mv_run[R], l_run[R], o[R], al_o[R];
+      // o is in units of 2^unit (l too, in the per-head modes); top: the largest unit that a tile has had.  Lane r of every
+      // warp keeps row r's; in the per-token modes lane R + r does, and lane r the maximum of x, which is l's unit.
+      float unit = -INFINITY, top = -INFINITY;
+      const bool unit_lane = !TOK || lane >= R;
+      float l_run[R], o[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        m_run[r] = mv_run[r] = -INFINITY;
-        l_run[r] = o[r] = 0.0f;
-        al_o[r] = 1.0f;
-      }
+      for (int r = 0; r < R; ++r) l_run[r] = o[r] = 0.0f;
       if (run.t0 < run.t1) {
         // ---- Q digits: D / 16 lanes a row, 16 values each
         constexpr int LPR = HD / 16;
@@ -361,9 +371,6 @@ __global__ void __launch_bounds__(DT, 2)
         mbar_arrive(&bar[B_Q]);
         ok = wait(B_Q, piece, 221);
       }
-      float f[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) f[r] = rowf[r];
       const int lim_lo = p.causal ? s.n - s.m : s.n - 1;  // every row sees the keys up to here
       // per-token scales of this thread's key, one tile ahead; its page two tiles ahead
       float sk = 0.0f, sv = 0.0f, sk_n = 0.0f, sv_n = 0.0f;
@@ -414,47 +421,52 @@ __global__ void __launch_bounds__(DT, 2)
         if (TOK) sk = finite_or_nan(sk);
         float x[R];
         const float lsv = TOK ? log2f(v_bad ? 0.0f : sv) : 0.0f;
+        float mx = -INFINITY;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          x[r] = join_digits<FP8>(a[r], a[R + r], a[2 * R + r]) * f[r];
+          x[r] = join_digits<FP8>(a[r], a[R + r], a[2 * R + r]) * rowf[r];
           if (TOK) x[r] *= sk;
           if (masked && key > rowl[r]) x[r] = -INFINITY;
-          const float mx = warp_max(x[r]);
-          const float mt = TOK ? warp_max(x[r] + lsv) : mx;
-          if (lane == 0) {
-            red[(bb * 4 + wg) * 2 * R + r] = mx;
-            if (TOK) red[(bb * 4 + wg) * 2 * R + R + r] = mt;
+          const float m = warp_max(x[r]);
+          if (lane == r) mx = m;
+          if (TOK) {
+            const float m2 = warp_max(x[r] + lsv);
+            if (lane == R + r) mx = m2;
           }
         }
+        if (lane < JOBS) red[(bb * 4 + wg) * JOBS + lane] = mx;
         mbar_arrive(&bar[B_RED + bb]);
         if (!(ok = wait(B_RED + bb, j >> 1, 224))) break;
-        // ---- p into the sums, the digits of w = p s_v 2^(m - mv)
+        // ---- p into the sums, the digits of w = s_v 2^(x - unit)
         if (L::NP == 1 || j >= 2) {
           // the P buffer is free once the P V that read it is done
           const int jp = L::NP == 1 ? j - 1 : j - 2;
           if (jp >= 0 && !(ok = wait(B_OF + (jp & 1), jp >> 1, 225))) break;
         }
         uint8_t* sp = smem + L::P + (L::NP == 2 ? bb : 0) * N * 128;
-        float al_new[R];
+        if (lane < JOBS) {
+          // the tile's unit: the largest weight of its keys as a power of two, but not kFall below the largest so far
+          const float* rd = red + bb * 4 * JOBS + lane;
+          float c = fmaxf(fmaxf(fmaxf(rd[0], rd[JOBS]), fmaxf(rd[2 * JOBS], rd[3 * JOBS])), -INFINITY);
+          if (unit_lane) c = ceilf(c);
+          top = fmaxf(top, c);
+          const float un = unit_lane ? fmaxf(c, top - kFall) : top, base = un == -INFINITY ? 0.0f : un;
+          const float al = attn::ex2(unit - base);  // of a unit: a whole power; 0 from -inf
+          unit = un;
+          if (unit_lane) alb[(bb * 4 + wg) * R + lane % R] = al;
+          reinterpret_cast<float2*>(units + wg * R + lane % R)[TOK && !unit_lane] = make_float2(base, al);
+        }
+        __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float* rd = red + bb * 4 * 2 * R + r;
-          const float mn = fmaxf(m_run[r], fmaxf(fmaxf(rd[0], rd[2 * R]), fmaxf(rd[4 * R], rd[6 * R])));
-          const float base = mn == -INFINITY ? 0.0f : mn;
-          const float pr = attn::ex2(x[r] - base);
-          l_run[r] = l_run[r] * (mn == m_run[r] ? 1.0f : attn::ex2(m_run[r] - mn)) + pr;
-          m_run[r] = mn;
-          float w = pr;
+          const float4 u = units[wg * R + r];
+          float w = attn::ex2((TOK ? x[r] + lsv : x[r]) - u.x);
           if (TOK) {
-            const float* rv = rd + R;
-            const float vn = fmaxf(mv_run[r], fmaxf(fmaxf(rv[0], rv[2 * R]), fmaxf(rv[4 * R], rv[6 * R])));
-            al_new[r] = vn == mv_run[r] ? 1.0f : attn::ex2(mv_run[r] - vn);
-            mv_run[r] = vn;
+            l_run[r] = l_run[r] * u.w + attn::ex2(x[r] - u.z);
             // not p s_v: p may vanish where s_v is large; a masked key, or one whose s_v is no number, has weight 0 here
-            w = vn == -INFINITY || !(x[r] > -INFINITY) || v_bad ? 0.0f : attn::ex2(x[r] + lsv - vn);
+            if (!(x[r] > -INFINITY) || v_bad) w = 0.0f;
           } else {
-            al_new[r] = mn == mv_run[r] ? 1.0f : attn::ex2(mv_run[r] - base);
-            mv_run[r] = mn;
+            l_run[r] = l_run[r] * u.y + w;
           }
           uint32_t d[3];
           p_digits<FP8>(w, d);
@@ -477,10 +489,8 @@ __global__ void __launch_bounds__(DT, 2)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[B_OE + jb]);
 #pragma unroll
-          for (int r = 0; r < R; ++r) o[r] = o[r] * al_o[r] + join_digits<FP8>(a[r], a[R + r], a[2 * R + r]);
+          for (int r = 0; r < R; ++r) o[r] = o[r] * alb[(jb * 4 + wg) * R + r] + join_digits<FP8>(a[r], a[R + r], a[2 * R + r]);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) al_o[r] = al_new[r];
       }
       if (!ok) break;
       // ---- the piece's end: its last O^T, the row sums, the result
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(DT, 2)
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          o[r] = o[r] * al_o[r] + join_digits<FP8>(a[r], a[R + r], a[2 * R + r]);
+          o[r] = o[r] * alb[(jb * 4 + wg) * R + r] + join_digits<FP8>(a[r], a[R + r], a[2 * R + r]);
           // every key's thread has noted its NaN codes before the last tile's maxima
           if (FP8 && nan_key[i] <= rowl[r]) o[r] = __uint_as_float(0x7FC00000u);
           if (TOK) lim[r] = rowl[r];  // (read before B_SUM: the next piece's limits come after it)
@@ -524,20 +534,26 @@ __global__ void __launch_bounds__(DT, 2)
           l_run[r] = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
         }
       }
+      // (mv, o's factor) and, in the per-token modes, (m, 1): o and the per-head l in units of 2^mv
+      if (lane < JOBS)
+        reinterpret_cast<float2*>(units + wg * R + lane % R)[TOK && !unit_lane] =
+            make_float2(top, top == -INFINITY ? 1.0f : attn::ex2(unit - top));
+      __syncwarp();
       const bool whole = run.u == run.it.first && run.it.first + run.it.nt <= run.u1;
       const int slot = 2 * blockIdx.x + (run.u == run.u0 ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= rows || half) break;
-        const float val = o[r] * kPUnit<FP8>;
+        const float4 u = units[wg * R + r];
+        const float val = o[r] * u.y * kPUnit<FP8>, m = TOK ? u.z : u.x, l = TOK ? l_run[r] : l_run[r] * u.y;
         if (whole) {
           const int ii = r / p.G;
           const long long row = (long long)(s.q0 + ii) * p.Hq + hk * p.G + r - ii * p.G;
-          p.out[row * HD + i] = __float2bfloat16(val * row_factor(p, hk, l_run[r], m_run[r], mv_run[r]));
-          if (i == 0 && p.lse) p.lse[row] = row_lse(l_run[r], m_run[r]);
+          p.out[row * HD + i] = __float2bfloat16(val * row_factor(p, hk, l, m, u.x));
+          if (i == 0 && p.lse) p.lse[row] = row_lse(l, m);
         } else {
           p.part_o[((long long)slot * DPL::RB + r) * HD + i] = val;
-          if (i == 0) p.part_ml[(long long)slot * DPL::RB + r] = make_float4(m_run[r], l_run[r], mv_run[r], 0.0f);
+          if (i == 0) p.part_ml[(long long)slot * DPL::RB + r] = make_float4(m, l, u.x, 0.0f);
         }
       }
     } while (ok && run.next(p));

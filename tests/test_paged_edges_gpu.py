@@ -188,3 +188,82 @@ def test_scales_of_a_head_that_are_no_numbers(faq, rows, mode, value):
             assert_within(z[~hit], lse[~hit], ltol[~hit], "lse")
         else:
             assert_within(z, lse, ltol, "lse")
+
+
+def sink_and_tail(mode, n, D):
+    """One sequence of n tokens: the first one's scores lie 17.5 (natural) above the others', which are equal; its V is zero,
+    theirs lie in [1, 1.98].  (cache, table, softmax scale for queries of ones)"""
+    page = 128
+    table, pages = ref.make_table((n,), page, 1)
+    c = ref.make_cache(mode, "BNSD", pages, 1, page, D, 2)
+    c["kc"].zero_()
+    v = torch.randint(50, 100, c["vc"].shape, generator=torch.Generator().manual_seed(3))
+    c["vc"] = ref.e4m3(v.float()) if mode.startswith("fp8") else v.to(torch.int8)
+    c["ks"].fill_(0.01), c["vs"].fill_(0.02)
+    pg, o = slot(table, page, 0)
+    put(c, "k", pg, 0, o, int(ref.e4m3(torch.tensor(64.0))) if mode.startswith("fp8") else 64)
+    put(c, "v", pg, 0, o, 0)
+    return c, table, 17.5 / (D * 64 * 0.01)
+
+
+@pytest.mark.parametrize("group", [1, 8, 16])
+@pytest.mark.parametrize("mode", ref.MODES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_flat_tail_under_one_large_weight(faq, group, mode, D):
+    """The first token takes nearly all of the weight and has a zero V; the others, each 2^-25 of it, are all of the output.
+    Many sequences read the same pages, so that a CTA's run of keys is long."""
+    n, B = 16384, 300
+    c, table1, scale = sink_and_tail(mode, n, D)
+    q = torch.ones(B, group, D, dtype=torch.bfloat16)
+    table, lens = table1.expand(B, -1).contiguous(), (n,) * B
+    want, lse, _, ltol = ref.attend(q[:1], c, table1, (n,), (1,), True, scale)
+    out, z = attend(faq, q, c, table, lens, (1,) * B, softmax_scale=scale)
+    # The tokens of the first token's tile (127) are held against it: each is off by at most 2^-24 of the largest weight
+    # (1 to nine digits), times its value (at most 104 * 0.02: 99 as E4M3).  The others are held against their own
+    # tile's largest: 2^-11 of each (and the scores' roundings, below 2^-18), and bf16's half step 2^-8.
+    tol = want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) + 127 * 2.0 ** -24 * 104 * 0.02
+    assert (tol < 0.05 * want.abs()).all()  # the bound says something
+    assert_within(out, want.expand(B, -1, -1), tol.expand(B, -1, -1), "out")
+    assert_within(z, lse.expand(B, -1), ltol.expand(B, -1), "lse")
+
+
+@pytest.mark.parametrize("rows", [20, 200])
+@pytest.mark.parametrize("mode", ref.MODES)
+def test_a_flat_tail_under_one_large_weight_of_a_chunk(faq, rows, mode):
+    """As above for more rows: weights are fp16 of 2^7 of the row's largest, whose steps end at 2^-24: each is off by at most
+    2^-32 of the largest."""
+    n, D = 16384, 128
+    c, table, scale = sink_and_tail(mode, n, D)
+    q = torch.ones(rows, 2, D, dtype=torch.bfloat16)
+    want, lse, _, ltol = ref.attend(q[:1], c, table, (n,), (1,), False, scale)
+    out, z = attend(faq, q, c, table, (n,), (rows,), causal=False, softmax_scale=scale)
+    tol = want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) + n * 2.0 ** -32 * 104 * 0.02
+    assert (tol < 0.05 * want.abs()).all()
+    assert_within(out, want.expand(rows, -1, -1), tol.expand(rows, -1, -1), "out")
+    assert_within(z, lse.expand(rows, -1), ltol.expand(rows, -1), "lse")
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("mode", ref.MODES)
+def test_tiles_far_apart(faq, rows, mode):
+    """Keys' scores that step up and down by hundreds from tile to tile: a tile far below the largest adds nothing and
+    disturbs nothing, in either order."""
+    n, page, D, B = 8192, 128, 64, 40
+    for kind in ("up", "down", "saw"):
+        table1, pages = ref.make_table((n,), page, 1)
+        c = ref.make_cache(mode, "BNSD", pages, 1, page, D, 5)
+        c["kc"].zero_()
+        c["ks"].fill_(1.0)
+        tiles = n // page
+        level = {"up": list(range(tiles)), "down": list(range(tiles))[::-1], "saw": [(t * 37) % tiles for t in range(tiles)]}[kind]
+        for t, x in enumerate(level):
+            put_code = int(ref.e4m3(torch.tensor(float(x)))) if mode.startswith("fp8") else x
+            pgs = int(table1[0, t])
+            c["kc"][pgs, 0, :, 0] = put_code
+        q = torch.zeros(B * rows, 2, D, dtype=torch.bfloat16)
+        q[..., 0] = 1.0
+        table = table1.expand(B, -1).contiguous()
+        want, lse, tol, ltol = ref.attend(q[:rows], c, table1, (n,), (rows,), True, 100.0)
+        out, z = attend(faq, q, c, table, (n,) * B, (rows,) * B, softmax_scale=100.0)
+        assert_within(out, want.repeat(B, 1, 1), tol.repeat(B, 1, 1), kind)
+        assert_within(z, lse.repeat(B, 1), ltol.repeat(B, 1), kind)

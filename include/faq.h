@@ -473,7 +473,9 @@ FAQ_API size_t fa_paged_attention_workspace_size(const fa_rows* q, const fa_page
  *       exp(softmax_scale * q_ir . (s_k k_j) - lse_ir),
  *   acc[b][h][j] = w, or acc[b][h][j] + w with accumulate != 0.
  *   q, causal, softmax_scale as fa_paged_attention's; lse: device fp32
- *   [T, Hq], what that call returned (rows at -inf give nothing).
+ *   [T, Hq], what that call returned.  A row whose lse is not finite (it saw
+ *   no key, was NaN, or the caller takes it out) gives nothing, whatever its
+ *   query and the keys hold.
  *   acc: device fp32 [B, Hkv, acc_stride]; acc_stride (tokens) must hold the
  *   longest sequence (longer ones are left out: FA_ERR_BOUNDS).  Entries at
  *   and past n_b are left as they were.  Sums are in a fixed order.

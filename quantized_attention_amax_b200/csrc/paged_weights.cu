@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + W_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* out_rows = reinterpret_cast<int*>(tmem_slot + 2);  // [2]: a walk's rows hold one that gives nothing
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // ---- the run: units [total c / grid, total (c + 1) / grid)
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
     }
     mbar_init(&bar[W_FIN], 1);
     *abort_flag = 0;
+    out_rows[0] = out_rows[1] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -271,8 +273,11 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
         const int here = min(rows - w * L::ROWS, L::ROWS), groups = (here + R - 1) / R;
         for (int idx = wt; idx - lane < groups * R * LPR; idx += 256) {
           const int rl = idx / LPR, c = idx % LPR, r = w * L::ROWS + rl, ii = r / p.G;
-          const bool in = idx < groups * R * LPR, live = in && r < rows;
+          const bool in = idx < groups * R * LPR, mine = in && r < rows;
           const int hq = hk * p.G + r - ii * p.G;
+          // a row whose LSE is not finite gives nothing, whatever its query and the keys hold
+          const float lse = mine ? __ldg(p.lse + (long long)(s.q0 + ii) * p.Hq + hq) : -INFINITY;
+          const bool live = fabsf(lse) < INFINITY;
           const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride + (long long)hq * D + c * 16);
           uint4 raw[2];
           raw[0] = live ? __ldg(src) : make_uint4(0, 0, 0, 0);
@@ -308,10 +313,10 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
                 make_uint4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
           }
           if (c == 0) {
-            const float lse = live ? __ldg(p.lse + (long long)(s.q0 + ii) * p.Hq + hq) : -INFINITY;
             RowC rc;
             rc.f = p.scale_log2 * inv;
-            rc.lim = lse == -INFINITY ? -1 : row_limit(p, s, r);
+            rc.lim = live ? row_limit(p, s, r) : -1;
+            if (mine && rc.lim < 0) out_rows[nq & 1] = 1;
             // log2(e) lse in two terms: log2(e) is 1.442695... as fp32 plus its remainder; rows that give
             // nothing: so far down that every exponential is 0
             rc.hi = rc.lim < 0 ? 1e30f : lse * 1.44269502f;
@@ -322,6 +327,8 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
         fence_async_smem();
         mbar_arrive(&bar[W_Q]);
         if (!(ok = wwait(W_Q, nq, 266))) break;
+        const bool some_out = out_rows[nq & 1] != 0;
+        if (wt == 0) out_rows[(nq + 1) & 1] = 0;  // read in the walk before, written in the next
         const int lim_lo = p.causal ? s.n - s.m + w * L::ROWS / p.G : s.n - 1;  // every row of the walk sees the keys up to here
         // ---- this warpgroup's tiles
         float sk_next = 0.0f;
@@ -339,7 +346,8 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
           sk_next = TOK ? load_scale(t + 2) : sk;
           const bool add = wp.accumulate || w > 0;
           const float old = add && key < s.n ? acc[key] : 0.0f;
-          const bool masked = t * TK + TK - 1 > lim_lo;
+          // (rows that pad a group need no mask of their own: a key that makes them NaN makes a row that sees it NaN)
+          const bool masked = some_out || t * TK + TK - 1 > lim_lo;
           float sum[2] = {0.0f, 0.0f};
           for (int g = 0; g < groups && ok; g += L::GS, ++steps) {
             if (!(ok = wwait(W_SF + x, steps, 267))) break;

@@ -267,3 +267,44 @@ def test_tiles_far_apart(faq, rows, mode):
         out, z = attend(faq, q, c, table, (n,) * B, (rows,) * B, softmax_scale=100.0)
         assert_within(out, want.repeat(B, 1, 1), tol.repeat(B, 1, 1), kind)
         assert_within(z, lse.repeat(B, 1), ltol.repeat(B, 1), kind)
+
+
+@pytest.mark.parametrize("qlen,Hq", [(1, 1), (1, 3), (2, 8), (30, 8)])
+@pytest.mark.parametrize("mode", ref.MODES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("out_by", [-INF, NAN, INF])
+def test_rows_without_a_finite_lse_give_nothing(faq, qlen, Hq, mode, causal, out_by):
+    """A row that the caller takes out by its LSE, or whose attention was NaN, adds nothing to any key, also where its query
+    or a key is no number, in tiles that every row sees whole too.  The other rows' weights are as ever."""
+    n = 700
+    lens, qlens = (n,), (qlen,)
+    table, pages = ref.make_table(lens, 32, 2)
+    c = ref.make_cache(mode, "BNSD", pages, 1, 32, 128, 3, spread=0.5)
+    q = bf16((qlen, Hq, 128), 4)
+    _, lse, _, _ = ref.attend(q, c, table, lens, qlens, causal)
+    lse = lse.float()
+    off = torch.zeros(qlen, Hq, dtype=torch.bool)
+    off[qlen // 2, Hq // 2] = True
+    ref_lse = torch.where(off, -INF, lse)
+    w, tol = ref.weigh(q, ref_lse, c, table, lens, qlens, causal, n)
+    lse[off] = out_by
+    for value in (1.0, NAN, INF):
+        bad_q = q.clone()
+        bad_q[off] = bad_q[off] * value
+        acc = torch.full((1, 1, n), 3.0).cuda()
+        faq.paged_weights(bad_q.cuda(), lse.cuda(), to_gpu(faq, c), batch_of(faq, table, lens, qlens), acc, causal=causal)
+        faq.check_device_status()
+        assert_within(acc, w + 3.0, tol + (w + 3.0) * 2.0 ** -24, "weights")
+    # every row taken out, a key whose K is NaN: nothing is added anywhere
+    pg, o = slot(table, 32, 40)
+    if mode.startswith("fp8"):
+        put(c, "k", pg, 0, o, (3, 0x7F))
+    elif mode not in ref.PER_HEAD:
+        c["ks"][pg, 0, o] = NAN
+    else:
+        c["ks"][0] = INF
+    acc = torch.full((1, 1, n), 3.0).cuda()
+    faq.paged_weights(q.cuda(), torch.full_like(lse, out_by).cuda(), to_gpu(faq, c), batch_of(faq, table, lens, qlens), acc,
+                      causal=causal)
+    faq.check_device_status()
+    assert (acc == 3.0).all()

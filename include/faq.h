@@ -415,8 +415,10 @@ FAQ_API fa_status fa_rope_table(float* table, int positions, int rotary_dim, con
  *   row holding a NaN gets a NaN scale and zero codes.  The per-head modes
  *   need amax_k, amax_v (device fp32 [H], FA_ERR_NO_CALIBRATION if NULL) and,
  *   with T > 0, (re)write the cache's scales with amax / 127 or amax / 448.
- *   q, q_out: rows of one T, H and D; q_out may be q (in place).  Both NULL:
- *   K and V only.  A page written by this call must not be another
+ *   q, q_out: rows of one T, H and D; q_out may be q (in place), and must not
+ *   overlap q, k or v otherwise (columns of one matrix side by side do not;
+ *   ranges that cross at two strides count as overlapping: FA_ERR_INVALID_ARG).
+ *   Both NULL: K and V only.  A page written by this call must not be another
  *   sequence's page too.
  */
 FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_paged_cache* cache,
@@ -437,7 +439,7 @@ FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_ro
  *   workspace: fa_paged_attention_workspace_size() bytes, 256-byte aligned
  *   (FA_ERR_WORKSPACE otherwise); only used during the call's kernels, so
  *   calls that can overlap (two streams) need one each.
- *   out must not overlap q.
+ *   q, out, lse and the workspace must not overlap (FA_ERR_INVALID_ARG).
  *   Scores, maxima, sums and accumulators are fp32.  Sequences of at most 16
  *   query rows per kv head (m_b * Hq / Hkv): Q and the probabilities (times
  *   s_v, per token) enter the products as sums of three 8-bit terms.  INT8: Q
@@ -478,7 +480,8 @@ FAQ_API size_t fa_paged_attention_workspace_size(const fa_rows* q, const fa_page
  *   query and the keys hold.
  *   acc: device fp32 [B, Hkv, acc_stride]; acc_stride (tokens) must hold the
  *   longest sequence (longer ones are left out: FA_ERR_BOUNDS).  Entries at
- *   and past n_b are left as they were.  Sums are in a fixed order.
+ *   and past n_b are left as they were.  acc must not overlap q or lse
+ *   (FA_ERR_INVALID_ARG).  Sums are in a fixed order.
  */
 FAQ_API fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_paged_cache* cache,
                                    const fa_paged_batch* batch, int causal, float softmax_scale, float* acc,
@@ -495,8 +498,9 @@ FAQ_API fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_
  *   Kept rows (codes, and the per-token modes' scales) move, in order, to
  *   cache indices 0, 1, ... of the same pages; rows at and past new_lens[b]
  *   are left as they were, and the pages that only they used are free.
- *   scores_out: nullable, device fp32 like scores (not the same buffer): the
- *   kept tokens' scores in order, then 0.  batch->cu_q is not used.  Keys
+ *   scores_out: nullable, device fp32 like scores: the kept tokens' scores in
+ *   order, then 0.  The outputs must not overlap each other, scores, seq_lens
+ *   or page_table (FA_ERR_INVALID_ARG).  batch->cu_q is not used.  Keys
  *   keep the rotation of their first positions, so later tokens need explicit
  *   positions in fa_rope_append.  A page must not be in two sequences.
  *   budget: 1 to 2^30 (above: FA_ERR_UNSUPPORTED); sink + recent <= budget.

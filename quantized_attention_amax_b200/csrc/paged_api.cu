@@ -47,6 +47,35 @@ fa_status check_rows(const fa_rows* r, int D) {
   return FA_OK;
 }
 
+// Do two ranges of bytes share any?
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// Do rows share bytes with a dense range?  Row i of r is [x + i s, x + i s + w): is there an i with both x + i s below
+// the range's end and its own end above the range's start.
+bool overlap(const fa_rows* r, const void* b, long long nb) {
+  const long long s = r->stride * 2, w = (long long)r->H * r->D * 2;
+  if (r->T < 1 || !overlap(r->data, (r->T - 1) * s + w, b, nb)) return false;
+  const long long from = (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(r->data));
+  const long long i = from < w ? 0 : (from - w) / s + 1;  // the first row that ends past the range's start
+  return i < r->T && i * s < from + nb;
+}
+
+// Do two sets of rows?  With one stride, columns side by side of one matrix do not; with two, ranges that cross count.
+bool overlap(const fa_rows* a, const fa_rows* b) {
+  const long long s = a->stride * 2, wa = (long long)a->H * a->D * 2, wb = (long long)b->H * b->D * 2;
+  if (a->T < 1 || b->T < 1) return false;
+  if (a->T == 1) return overlap(b, a->data, wa);
+  if (b->T == 1) return overlap(a, b->data, wb);
+  if (!overlap(a->data, (a->T - 1) * s + wa, b->data, (b->T - 1) * b->stride * 2 + wb)) return false;
+  if (a->stride != b->stride) return true;
+  const long long d = (long long)(reinterpret_cast<uintptr_t>(b->data) - reinterpret_cast<uintptr_t>(a->data));
+  const long long m = ((d % s) + s) % s;  // where a row of b starts in a row of a
+  return m < wa || m + wb > s;
+}
+
 // Largest cached length is kept in 32 bits: the table's tokens must fit.
 bool lengths_fit(const fa_paged_cache* c, const fa_paged_batch* b) {
   return (long long)b->max_pages * c->page_size <= 0x40000000LL;
@@ -95,6 +124,8 @@ fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, c
     if ((st = check_rows(q_out, cache->D)) != FA_OK) return st;
     if (q->T != k->T || q_out->T != q->T || q_out->H != q->H) return FA_ERR_INVALID_ARG;
     if (q->data == q_out->data && q->stride != q_out->stride) return FA_ERR_INVALID_ARG;
+    // in place, or apart: other warps read what a row of q_out lies on
+    if ((q->data != q_out->data && overlap(q, q_out)) || overlap(k, q_out) || overlap(v, q_out)) return FA_ERR_INVALID_ARG;
   }
   if (!batch->cu_q && k->T != batch->B) return FA_ERR_INVALID_ARG;
   if (rotary_dim < 0 || rotary_dim > cache->D || rotary_dim % 16 != 0 || table_positions < 0) return FA_ERR_INVALID_ARG;
@@ -123,8 +154,14 @@ fa_status fa_paged_attention(const fa_rows* q, const fa_paged_cache* cache, cons
   if (st != FA_OK) return st;
   if (q->T == 0 || batch->B == 0) return FA_OK;
   if (!out || !aligned(out, 16) || !aligned(lse, 4)) return FA_ERR_INVALID_ARG;
+  // rows of q are read after others' results are written
+  const long long n_out = (long long)q->T * q->H * q->D * 2, n_lse = (long long)q->T * q->H * 4;
+  if (overlap(q, out, n_out) || overlap(q, lse, n_lse) || overlap(out, n_out, lse, n_lse)) return FA_ERR_INVALID_ARG;
   PagedAttnArgs a = {q, cache, batch, causal ? 1 : 0, softmax_scale, out, lse, nullptr, nullptr, 0, 0};
-  if (!workspace || ws_bytes < paged_attention_ws(a) || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
+  const long long n_ws = (long long)paged_attention_ws(a);
+  if (!workspace || ws_bytes < (size_t)n_ws || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
+  if (overlap(q, workspace, n_ws) || overlap(out, n_out, workspace, n_ws) || overlap(lse, n_lse, workspace, n_ws))
+    return FA_ERR_INVALID_ARG;
   a.status = device_status_ptr();
   if (!a.status) return FA_ERR_CUDA;
   return from_cuda(launch_paged_attention(a, workspace, reinterpret_cast<cudaStream_t>(s)));
@@ -138,6 +175,8 @@ fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_paged_ca
   if (acc_stride < 0) return FA_ERR_INVALID_ARG;
   if (batch->B == 0 || (q->T == 0 && accumulate)) return FA_OK;  // (no new token: the weights are zero)
   if ((q->T > 0 && !lse) || !aligned(lse, 4) || (acc_stride > 0 && !acc) || !aligned(acc, 4)) return FA_ERR_INVALID_ARG;
+  const long long n_acc = (long long)batch->B * cache->H * acc_stride * 4;
+  if (overlap(q, acc, n_acc) || overlap(lse, (long long)q->T * q->H * 4, acc, n_acc)) return FA_ERR_INVALID_ARG;
   int* status = device_status_ptr();
   if (!status) return FA_ERR_CUDA;
   const PagedAttnArgs a = {q,   cache, batch,      causal ? 1 : 0, softmax_scale, nullptr, const_cast<float*>(lse), status,
@@ -157,8 +196,20 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const fa_paged_batch* batc
   if (!lengths_fit(cache, batch) || budget > 0x40000000) return FA_ERR_UNSUPPORTED;
   if (batch->B == 0) return FA_OK;
   if ((score_stride > 0 && !scores) || !aligned(scores, 4) || !kept || !aligned(kept, 4) || !new_lens ||
-      !aligned(new_lens, 4) || !aligned(scores_out, 4) || (scores && scores == scores_out))
+      !aligned(new_lens, 4) || !aligned(scores_out, 4))
     return FA_ERR_INVALID_ARG;
+  // the outputs lie apart from each other and from what other CTAs still read (new_lens is not seq_lens)
+  const long long items = (long long)batch->B * cache->H, n_sc = items * score_stride * 4, n_kept = items * budget * 4;
+  const long long n_b = (long long)batch->B * 4, n_tab = n_b * batch->max_pages;
+  const void* outs[3] = {scores_out, kept, new_lens};
+  const long long n_out[3] = {n_sc, n_kept, n_b};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(outs[i], n_out[i], scores, n_sc) || overlap(outs[i], n_out[i], batch->seq_lens, n_b) ||
+        overlap(outs[i], n_out[i], batch->page_table, n_tab))
+      return FA_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (overlap(outs[i], n_out[i], outs[k], n_out[k])) return FA_ERR_INVALID_ARG;
+  }
   int* status = device_status_ptr();
   if (!status) return FA_ERR_CUDA;
   const PagedEvictArgs a = {cache, batch, scores, score_stride, budget, sink, recent, kept, new_lens, scores_out, status};

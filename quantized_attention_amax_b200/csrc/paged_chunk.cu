@@ -374,12 +374,13 @@ __global__ void __launch_bounds__(CT, 1)
       int raw_page = -1;           // its page in the tile after that, as it lies in the table
       auto load_page = [&](int t) {
         const int key = t * TN + ct;
-        return t < t1 && key < n ? __ldg(p.bt.table + (long long)b * p.bt.max_pages + (key >> p.c.page_shift)) : -1;
+        return t < t1 && key < n && in_bounds(key >= 0 && (key >> p.c.page_shift) < p.bt.max_pages, 181) ? __ldg(p.bt.table + (long long)b * p.bt.max_pages + (key >> p.c.page_shift)) : -1;
       };
       auto load_scales = [&](int t, int pg) {
         sk = sv = 0.0f;
         if ((unsigned)pg < (unsigned)p.c.pages) {
           const long long si = p.c.scale(pg, hk, (t * TN + ct) & p.c.page_mask);
+          if (!p.c.holds_scale(si, 182)) return;
           sk = __ldg(p.c.ks + si);
           sv = __ldg(p.c.vs + si);
         }
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(CT, 1)
         // ---- this thread's Q row as fp16, scaled by a power of two
         const Seq s = {pc.q0, pc.m, pc.n};
         const int hk = pc.hk, r = pc.row0 + i + (dual ? 0 : x * BM), ii = r / p.G;
-        const bool live = r < s.m * p.G;
+        const bool live = r < s.m * p.G && q_row_ok(p, s, hk, r, 183);
         lim = live ? row_limit(p, s, r) : -1;
         warp_live = __any_sync(0xffffffffu, live);
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride +
@@ -757,7 +758,8 @@ __global__ void __launch_bounds__(CT, 1)
         const bool any_b = dual && n_b > 0;
         const bool whole = pc.whole;
         const int hk = pc.hk, r = pc.row0 + i + (dual ? 0 : x * BM), ii = r / p.G;
-        const bool live = r < pc.m * p.G;
+        const bool live = r < pc.m * p.G && q_row_ok(p, {pc.q0, pc.m, pc.n}, hk, r, 184) &&
+                          (whole || in_bounds(pc.slot < 2 * (int)gridDim.x && r - pc.row0 >= 0 && r - pc.row0 < PL::RB, 185));
         const long long slot_row = (long long)pc.slot * PL::RB + (r - pc.row0);
         const long long out_row = (long long)(pc.q0 + ii) * p.Hq + hk * p.G + r - ii * p.G;
         const float fac = whole ? row_factor(p, hk, l_run, m_ref, m_ref) : 1.0f;
@@ -842,6 +844,7 @@ size_t paged_chunk_ws(int D) { return plan_ws<CPL>(D, sm_count()); }
 
 cudaError_t launch_paged_chunk(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   AttnP p = paged_attn_params(a);
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   const int D = a.q->D, grid = sm_count();
   plan_carve<CPL>(p, ws, D, grid);
   CUtensorMap mk, mv;

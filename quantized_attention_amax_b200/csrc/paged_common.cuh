@@ -32,6 +32,13 @@ struct Cache {
   __device__ __forceinline__ long long scale(int pg, int h, int slot) const {
     return (((long long)pg * H + h) << page_shift) + slot;
   }
+  // FA_DEBUG_BOUNDS builds: `n` bytes of codes from `off`, and the per-token modes' scale `i`
+  __device__ __forceinline__ bool holds(long long off, int n, int where) const {
+    return in_bounds(off >= 0 && off + n <= (long long)pages * page_stride, where);
+  }
+  __device__ __forceinline__ bool holds_scale(long long i, int where) const {
+    return in_bounds(i >= 0 && i < (long long)pages * H * (page_mask + 1), where);
+  }
 };
 
 struct Batch {
@@ -53,6 +60,7 @@ struct Seq {
 };
 __device__ __forceinline__ Seq load_seq(const Batch& bt, int page_shift, int b, int* status, int where) {
   Seq s;
+  if (!in_bounds(b >= 0 && b < bt.B, 162)) return {0, 0, 0};
   s.q0 = bt.cu ? __ldg(bt.cu + b) : b;
   const int q1 = bt.cu ? __ldg(bt.cu + b + 1) : b + 1;
   s.n = __ldg(bt.lens + b);
@@ -68,6 +76,7 @@ __device__ __forceinline__ Seq load_seq(const Batch& bt, int page_shift, int b, 
 
 // Page of cache index j of sequence b, or -1 (recorded) if it is not a page of the cache.
 __device__ __forceinline__ int page_of(const Batch& bt, const Cache& c, int b, int j, int* status, int where) {
+  if (!in_bounds(b >= 0 && b < bt.B && j >= 0 && (j >> c.page_shift) < bt.max_pages, 161)) return -1;
   const int pg = __ldg(bt.table + (long long)b * bt.max_pages + (j >> c.page_shift));
   if ((unsigned)pg >= (unsigned)c.pages) {
     bad(status, where);

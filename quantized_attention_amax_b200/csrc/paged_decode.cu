@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(DT, 2)
         constexpr int LPR = HD / 16;
         for (int idx = i; idx - lane < R * LPR; idx += 128) {
           const int r = idx / LPR, c = idx % LPR, ii = r / p.G;
-          const bool live = r < R && r < rows;
+          const bool live = r < R && r < rows && q_row_ok(p, s, hk, r, 174);
           const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(s.q0 + ii) * p.q_stride +
                                                             (long long)(hk * p.G + r - ii * p.G) * HD + c * 16);
           uint4 raw[2];
@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(DT, 2)
       };
       auto load_scales = [&](int t, int pg, float& k, float& v) {
         const long long si = p.c.scale(pg, hk, (t * TK + i) & p.c.page_mask);
+        if (pg >= 0 && !p.c.holds_scale(si, 175)) pg = -1;
         k = pg >= 0 ? __ldg(p.c.ks + si) : 0.0f;
         v = pg >= 0 ? __ldg(p.c.vs + si) : 0.0f;
       };
@@ -549,9 +550,10 @@ __global__ void __launch_bounds__(DT, 2)
         if (whole) {
           const int ii = r / p.G;
           const long long row = (long long)(s.q0 + ii) * p.Hq + hk * p.G + r - ii * p.G;
+          if (!q_row_ok(p, s, hk, r, 176)) continue;
           p.out[row * HD + i] = __float2bfloat16(val * row_factor(p, hk, l, m, u.x));
           if (i == 0 && p.lse) p.lse[row] = row_lse(l, m);
-        } else {
+        } else if (in_bounds(slot < 2 * (int)gridDim.x && r < DPL::RB, 177)) {
           p.part_o[((long long)slot * DPL::RB + r) * HD + i] = val;
           if (i == 0) p.part_ml[(long long)slot * DPL::RB + r] = make_float4(m, l, u.x, 0.0f);
         }
@@ -602,6 +604,7 @@ size_t paged_decode_ws(int D) { return plan_ws<DPL>(D, 2 * sm_count()); }
 
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int rows, void* ws, cudaStream_t s) {
   AttnP p = paged_attn_params(a);
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   const int D = a.q->D, grid = 2 * sm_count();
   plan_carve<DPL>(p, ws, D, grid);
   CUtensorMap mk, mv;

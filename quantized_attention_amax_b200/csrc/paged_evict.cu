@@ -80,11 +80,17 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
   const int keep = min(n, p.budget);
   const int gt0 = rank * ET + tid, gts = cs * ET;  // the thread among the cluster's
   if (h == 0 && gt0 == 0) p.new_lens[b] = keep;
-  for (int i = keep + gt0; i < p.budget; i += gts) kept[i] = -1;
+  // the extents of this item's lists (FA_DEBUG_BOUNDS builds)
+  auto kept_ok = [&](long long i) { return in_bounds(i >= 0 && i < p.budget, 194); };
+  auto score_ok = [&](long long i) { return in_bounds(i >= 0 && i < p.score_stride, 195); };
+  for (int i = keep + gt0; i < p.budget; i += gts)
+    if (kept_ok(i)) kept[i] = -1;
   if (so)
-    for (long long i = keep + gt0; i < p.score_stride; i += gts) so[i] = 0.0f;
+    for (long long i = keep + gt0; i < p.score_stride; i += gts)
+      if (score_ok(i)) so[i] = 0.0f;
   if (n <= p.budget) {
     for (int i = gt0; i < n; i += gts) {
+      if (!kept_ok(i) || !score_ok(i)) continue;
       kept[i] = i;
       if (so) so[i] = __ldg(sc + i);
     }
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int i = i0 + q * ET + tid;
-      x[q] = i < cached ? __ldg(mine + i) : 0.0f;
+      x[q] = i < cached && score_ok(p.sink + lo + i) ? __ldg(mine + i) : 0.0f;
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -112,7 +118,7 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
       if (i < cached) keys[i] = score_bits(x[q]);
     }
   }
-  auto key = [&](int i) { return i < CAP ? keys[i] : score_bits(__ldg(mine + i)); };
+  auto key = [&](int i) { return i < CAP ? keys[i] : score_ok(p.sink + lo + i) ? score_bits(__ldg(mine + i)) : 0u; };
 
   uint32_t thr = 0;
   if (need > 0) {
@@ -210,18 +216,21 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
       const uint32_t e = eq_before + __popc(be & below);  // equal scores before this one
       if (is_gt || (is_eq && e < (uint32_t)need)) {
         const uint32_t place = gt_before + __popc(bg & below) + min(e, (uint32_t)need);
-        kept[p.sink + place] = p.sink + lo + i;
+        if (kept_ok((long long)p.sink + place)) kept[p.sink + place] = p.sink + lo + i;
       }
       gt_before += __popc(bg);
       eq_before += __popc(be);
     }
-  for (int i = gt0; i < p.sink; i += gts) kept[i] = i;
-  for (int i = gt0; i < p.recent; i += gts) kept[p.budget - p.recent + i] = n - p.recent + i;
+  for (int i = gt0; i < p.sink; i += gts)
+    if (kept_ok(i)) kept[i] = i;
+  for (int i = gt0; i < p.recent; i += gts)
+    if (kept_ok(p.budget - p.recent + i)) kept[p.budget - p.recent + i] = n - p.recent + i;
   cl.sync();  // the list is written; the slices' keys are read
 
   if (so)  // the kept tokens' scores
 #pragma unroll 4
-    for (int i = gt0; i < keep; i += gts) so[i] = __ldg(sc + __ldcg(kept + i));
+    for (int i = gt0; i < keep; i += gts)
+      if (score_ok(i) && score_ok(__ldcg(kept + i))) so[i] = __ldg(sc + __ldcg(kept + i));
 
   // ---- 3. the rows
   constexpr int CH = D / 16;               // 16-byte chunks per code row
@@ -244,7 +253,10 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
     }
     int pg[RU];
 #pragma unroll
-    for (int u = 0; u < RU; ++u) pg[u] = f[u] >= 0 ? __ldg(table + (f[u] >> p.c.page_shift)) : -1;
+    for (int u = 0; u < RU; ++u) {
+      if (!in_bounds(f[u] < n && ((d0 + u * RS) >> p.c.page_shift) >= 0, 196)) f[u] = -1;
+      pg[u] = f[u] >= 0 ? __ldg(table + (f[u] >> p.c.page_shift)) : -1;
+    }
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       if (f[u] >= 0 && (unsigned)pg[u] >= (unsigned)p.c.pages) {
@@ -253,6 +265,10 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
       }
       if (f[u] >= 0) {
         const int slot = f[u] & p.c.page_mask;
+        if (!p.c.holds(p.c.row(pg[u], h, slot) + 16 * cc, 16, 197) || !p.c.holds_scale(p.c.scale(pg[u], h, slot), 198)) {
+          f[u] = -1;
+          continue;
+        }
         row[u] = __ldcg(reinterpret_cast<const uint4*>(codes + p.c.row(pg[u], h, slot)) + cc);
         if (scales && cc == 0) scale[u] = __ldcg(scales + p.c.scale(pg[u], h, slot));
       }
@@ -271,6 +287,7 @@ __global__ void __launch_bounds__(ET, 1) paged_evict_kernel(const EvictP p) {
         continue;
       }
       const int slot = (d0 + u * RS) & p.c.page_mask;
+      if (!p.c.holds(p.c.row(pg[u], h, slot) + 16 * cc, 16, 197) || !p.c.holds_scale(p.c.scale(pg[u], h, slot), 198)) continue;
       reinterpret_cast<uint4*>(codes + p.c.row(pg[u], h, slot))[cc] = row[u];
       if (scales && cc == 0) scales[p.c.scale(pg[u], h, slot)] = scale[u];
     }
@@ -304,6 +321,7 @@ cudaError_t launch_d(const EvictP& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t s) {
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   EvictP p = {};
   p.c = paged_cache_of(*a.cache);
   p.bt = paged_batch_of(*a.batch, 0);

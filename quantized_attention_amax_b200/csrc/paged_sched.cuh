@@ -188,6 +188,11 @@ __device__ __forceinline__ float row_factor(const AttnP& p, int hk, float l, flo
   if (!(l > 0.0f) && l == l) return 0.0f;  // no key seen
   return (p.c.per_token ? attn::ex2(mv - m) : finite_or_nan(__ldg(p.c.vs + hk))) / l;
 }
+// FA_DEBUG_BOUNDS builds: row r of kv head hk of the sequence is a row of q
+__device__ __forceinline__ bool q_row_ok(const AttnP& p, const Seq& s, int hk, int r, int where) {
+  const int i = r / p.G, hq = hk * p.G + r - i * p.G;
+  return in_bounds(s.q0 >= 0 && i >= 0 && s.q0 + i < p.bt.T && hq >= 0 && hq < p.Hq, where);
+}
 __device__ __forceinline__ float row_lse(float l, float m) { return (m + log2f(l)) * 0.69314718055994530942f; }
 
 // Programmatic dependent launch: a kernel lets the one behind it start (its launch and prologue then overlap), which
@@ -247,7 +252,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
   for (int k0 = 0; k0 < pieces; k0 += CB) {
     const int n = min(CB, pieces - k0);
     __syncthreads();
-    for (int i = threadIdx.x; i < n * 16; i += 256) ml[i / 16][i % 16] = p.part_ml[row_of(k0 + i / 16, i % 16)];
+    for (int i = threadIdx.x; i < n * 16; i += 256)
+      if (in_bounds(row_of(k0 + i / 16, i % 16) < 2LL * grid * PL::RB, 171)) ml[i / 16][i % 16] = p.part_ml[row_of(k0 + i / 16, i % 16)];
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < NR; ++y) {
@@ -266,6 +272,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
 #pragma unroll 8
       for (int k = part; k < n; k += splits) {
         const float4 v = ml[k][r];
+        if (!in_bounds(row_of(k0 + k, r) < 2LL * grid * PL::RB, 172)) continue;
         const float4 x = *(reinterpret_cast<const float4*>(p.part_o + row_of(k0 + k, r) * D) + ch);
         // maxima pass over NaN, so a piece whose scores are all NaN has m = -inf, as one without keys has: its sum
         // tells them apart (NaN or 0) and enters as it is, and so do sums of p v (0, or NaN)
@@ -301,6 +308,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
     const int i = rr / p.G, hq = it.hk * p.G + rr - i * p.G;
     const float f = row_factor(p, it.hk, l[y], m[y], mv[y]);
     const long long row = (long long)(it.s.q0 + i) * p.Hq + hq;
+    if (!in_bounds(row >= 0 && row < (long long)p.bt.T * p.Hq, 173)) continue;
     const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[y].x * f, acc[y].y * f), v1 = __floats2bfloat162_rn(acc[y].z * f, acc[y].w * f);
     *reinterpret_cast<uint2*>(p.out + row * D + ch * 4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
@@ -311,6 +319,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnP p, int grid) {
 // The combine kernel behind a kernel of that plan that let it start.
 template <typename PL, int D>
 inline cudaError_t launch_combine(const AttnP& p, int grid, cudaStream_t s) {
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, PL::RB / 16);
   cfg.blockDim = dim3(256);

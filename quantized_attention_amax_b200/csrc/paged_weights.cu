@@ -261,8 +261,10 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
       const Seq s = run.s;
       const int hk = run.hk, b = run.b, rows = s.m * p.G, nw = walks();
       float* acc = wp.acc + ((long long)b * p.c.H + hk) * wp.acc_stride;
+      auto acc_ok = [&](int j) { return in_bounds(j >= 0 && j < wp.acc_stride && b >= 0 && b < p.bt.B && hk >= 0 && hk < p.c.H, 192); };
       if (nw == 0)  // no new token, not accumulating: zeros
-        for (int j = run.t0 * TK + wt; j < min(run.t1 * TK, s.n); j += 256) acc[j] = 0.0f;
+        for (int j = run.t0 * TK + wt; j < min(run.t1 * TK, s.n); j += 256)
+          if (acc_ok(j)) acc[j] = 0.0f;
       for (int w = 0; w < nw && ok; ++w, ++nq) {
         // ---- Q digits and the rows' constants, D / 16 lanes a row, once the MMAs of the walk before are done
         if (nq > 0) {
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
         const int here = min(rows - w * L::ROWS, L::ROWS), groups = (here + R - 1) / R;
         for (int idx = wt; idx - lane < groups * R * LPR; idx += 256) {
           const int rl = idx / LPR, c = idx % LPR, r = w * L::ROWS + rl, ii = r / p.G;
-          const bool in = idx < groups * R * LPR, mine = in && r < rows;
+          const bool in = idx < groups * R * LPR, mine = in && r < rows && q_row_ok(p, s, hk, r, 191);
           const int hq = hk * p.G + r - ii * p.G;
           // a row whose LSE is not finite gives nothing, whatever its query and the keys hold
           const float lse = mine ? __ldg(p.lse + (long long)(s.q0 + ii) * p.Hq + hq) : -INFINITY;
@@ -337,7 +339,8 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
           if (!TOK) return __ldg(p.c.ks + hk);
           if (t >= run.t1 || key >= s.n) return 0.0f;
           const int pg = page_of(p.bt, p.c, b, key, p.status, 223);
-          return pg >= 0 ? __ldg(p.c.ks + p.c.scale(pg, hk, key & p.c.page_mask)) : 0.0f;
+          const long long si = p.c.scale(pg, hk, key & p.c.page_mask);
+          return pg >= 0 && p.c.holds_scale(si, 193) ? __ldg(p.c.ks + si) : 0.0f;
         };
         if (run.t0 + x < run.t1) sk_next = load_scale(run.t0 + x);
         for (int t = run.t0 + x; t < run.t1 && ok; t += 2) {
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
           const float sk = sk_next;
           sk_next = TOK ? load_scale(t + 2) : sk;
           const bool add = wp.accumulate || w > 0;
-          const float old = add && key < s.n ? acc[key] : 0.0f;
+          const float old = add && key < s.n && acc_ok(key) ? acc[key] : 0.0f;
           // (rows that pad a group need no mask of their own: a key that makes them NaN makes a row that sees it NaN)
           const bool masked = some_out || t * TK + TK - 1 > lim_lo;
           float sum[2] = {0.0f, 0.0f};
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(WT, 1) paged_weights_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[W_SE + x]);
           }
-          if (ok && key < s.n) acc[key] = old + (sum[0] + sum[1]);
+          if (ok && key < s.n && acc_ok(key)) acc[key] = old + (sum[0] + sum[1]);
         }
       }
     } while (ok && run.next(wp));
@@ -423,6 +426,7 @@ cudaError_t launch_paged_weights(const PagedAttnArgs& a, cudaStream_t s) {
   p.accumulate = a.accumulate;
   p.acc = a.acc;
   p.acc_stride = a.acc_stride;
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   CUtensorMap mk;
   const cudaError_t e = make_page_map(&mk, a.cache->k_codes, *a.cache, TK, true);
   if (e != cudaSuccess) return e;

@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ tab
     const int i = (int)(idx - p * half);
     double sn, cs;
     sincos((double)p * inv.f[i], &sn, &cs);
+    if (!in_bounds(p * 2 * half + half + i < 2 * n, 167)) continue;
     table[p * 2 * half + i] = (float)(factor * cs);
     table[p * 2 * half + half + i] = (float)(factor * sn);
   }
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a) {
       const int r = r0 + u * RPW;
       const Rows& x = r < Hq ? a.q : r < Hq + a.c.H ? a.k : a.v;
       const int h = r < Hq ? r : r < Hq + a.c.H ? r - Hq : r - Hq - a.c.H;
-      ahead[u] = r < r_end ? *(reinterpret_cast<const uint4*>(x.p + (long long)t * x.stride + (long long)h * D) + gl)
+      const bool ok = r < r_end && in_bounds(t < a.bt.T && h >= 0 && h < x.H, 163);
+      ahead[u] = ok ? *(reinterpret_cast<const uint4*>(x.p + (long long)t * x.stride + (long long)h * D) + gl)
                            : make_uint4(0, 0, 0, 0);
     }
   };
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a) {
           }
         }
       }
-      if (live && is_q)
+      if (live && is_q && in_bounds(t < a.bt.T && r * D + 8 * gl + 8 <= a.qo_stride, 164))
         *(reinterpret_cast<uint4*>(a.qo + (long long)t * a.qo_stride + (long long)r * D) + gl) = raw[u];
       if (r - sub + RPW <= Hq) continue;  // no K or V row in this warp's rows: the same for every lane
       // ---- quantize the K or V row
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a) {
         const float lo = __uint_as_float(m2 << 16), hi = __uint_as_float(m2 & 0xFFFF0000u);
         sc = __fdiv_rn(lo != lo ? lo : hi != hi ? hi : fmaxf(lo, hi), QMAX);
       }
-      if (!kv || pg < 0) continue;
+      if (!kv || pg < 0 || !a.c.holds(a.c.row(pg, h, slot) + 8 * gl, 8, 165)) continue;
       unpack_bf16x8(raw[u], x);
       // x / s as IEEE division rounds it where that decides the code (quant_common.cuh)
       if (sc >= kFastDivMin && sc < INFINITY) {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a) {
       const uint2 o = INT8 ? make_uint2(s8x4<true>(x[0], x[1], x[2], x[3]), s8x4<true>(x[4], x[5], x[6], x[7]))
                            : make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
       *(reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + a.c.row(pg, h, slot)) + gl) = o;
-      if (!PER_HEAD && gl == 0) (is_v ? a.c.vs : a.c.ks)[a.c.scale(pg, h, slot)] = sc;
+      if (!PER_HEAD && gl == 0 && a.c.holds_scale(a.c.scale(pg, h, slot), 166)) (is_v ? a.c.vs : a.c.ks)[a.c.scale(pg, h, slot)] = sc;
     }
   }
 }
@@ -253,12 +255,14 @@ cudaError_t launch_rope_table(float* table, int positions, int rotary_dim, const
   for (int i = 0; i < rotary_dim / 2; ++i) f.f[i] = inv_freq[i];
   const long long n = (long long)positions * (rotary_dim / 2);
   if (n == 0) return cudaSuccess;
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   const long long want = (n + 255) / 256, cap = 16LL * sm_count();
   rope_table_kernel<<<(unsigned)(want < cap ? want : cap), 256, 0, s>>>(table, n, rotary_dim / 2, f, factor);
   return cudaGetLastError();
 }
 
 cudaError_t launch_rope_append(const RopeAppendArgs& r, cudaStream_t s) {
+  if (const cudaError_t be = bounds_attach(); be != cudaSuccess) return be;
   AppendArgs a = {};
   if (r.q) a.q = {static_cast<const __nv_bfloat16*>(r.q->data), r.q->stride, r.q->H};
   a.k = {static_cast<const __nv_bfloat16*>(r.k->data), r.k->stride, r.k->H};

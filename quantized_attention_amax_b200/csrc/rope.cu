@@ -65,17 +65,15 @@ struct AppendArgs {
   int* status;
 };
 
-// The sequence of row t: how many sequences end at or before it.  bt.B if none holds it.
+// The (first) sequence whose rows hold row t; bt.B if none does.
 __device__ __forceinline__ int seq_of_row(const Batch& bt, int t, int lane) {
   if (!bt.cu) return t < bt.B ? t : bt.B;
-  int n = 0;
   for (int b0 = 0; b0 < bt.B; b0 += 32) {
     const int b = b0 + lane;
-    const unsigned done = __ballot_sync(0xffffffffu, b < bt.B && __ldg(bt.cu + b + 1) <= t);
-    n += __popc(done);
-    if (done != 0xffffffffu) break;
+    const unsigned in = __ballot_sync(0xffffffffu, b < bt.B && __ldg(bt.cu + b) <= t && t < __ldg(bt.cu + b + 1));
+    if (in) return b0 + __ffs(in) - 1;
   }
-  return n;
+  return bt.B;
 }
 
 // a' = a cos - b sin, b' = b cos + a sin
@@ -96,6 +94,8 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendArgs a) {
   const int lane = threadIdx.x & 31;
   const int gl = lane % LPR, sub = lane / LPR;
   const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (blockIdx.x == 0)  // every sequence's check, of those too that no row leads to
+    for (int b = threadIdx.x; b < a.bt.B; b += blockDim.x) load_seq(a.bt, a.c.page_shift, b, a.status, 201);
   if (PER_HEAD && blockIdx.x == 0)
     for (int h = threadIdx.x; h < a.c.H; h += blockDim.x) {
       a.c.ks[h] = __fdiv_rn(__ldg(a.amax_k + h), QMAX);

@@ -308,3 +308,23 @@ def test_rows_without_a_finite_lse_give_nothing(faq, qlen, Hq, mode, causal, out
                       causal=causal)
     faq.check_device_status()
     assert (acc == 3.0).all()
+
+
+def test_an_append_with_offsets_that_fall(faq):
+    """Offsets that fall, and a bad length of a sequence without new tokens: reported by the append too, although no row leads
+    to those sequences, and the rows of the others are theirs."""
+    table, pages = ref.make_table((100, 60, 30), 16, 1)
+    k = bf16((6, 2, 64), 3).cuda()
+    for cu, lens in (((0, 2, 1, 1), (100, 60, 30)), ((0, 2, 2, 4), (100, -5, 30)), ((0, 2, 2, 4), (100, 2 ** 30, 30))):
+        c = ref.make_cache("int8_per_token", "BNSD", pages, 2, 16, 64, 2)
+        gc, want = to_gpu(faq, c), to_gpu(faq, c)
+        gb = faq.PagedBatch(table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), torch.tensor(cu, dtype=torch.int32).cuda())
+        faq.rope_append(None, k, k, gc, gb)
+        with pytest.raises(faq.FaqError) as e:
+            faq.check_device_status()
+        assert e.value.status == 8
+        fine = (0, 2, 2, 2 + max(0, cu[3] - cu[2]))
+        faq.rope_append(None, k, k, want, batch_of(faq, table, (100, 60, 30), [fine[i + 1] - fine[i] for i in range(3)]))
+        faq.check_device_status()
+        for a, b in ((gc.k_codes, want.k_codes), (gc.v_codes, want.v_codes), (gc.k_scales, want.k_scales), (gc.v_scales, want.v_scales)):
+            assert torch.equal(a, b)

@@ -13,11 +13,11 @@
 // pair a half with itself count.
 // A softmax thread owns a key of S^T and a dim of O^T (D = 64: of one half's).  Per tile: join the digits' sums into scores, the rows'
 // maxima over the 128 keys (warp reductions, then the four warps through shared memory), p = 2^(x - m) into the row
-// sums, and the digits of w = s_v 2^(x - u) for the second product (per-head modes: w = p, without s_v), 2^u the tile's
-// own largest weight brought up to a power of two: w is at most 1 whatever the scales' range, and the digits'
-// fixed step stays small beside a tile's weights, however far these lie below the row's largest (a long history's many
-// small weights would otherwise count in the row sum alone).  O is kept in registers, rescaled by whole powers of two
-// from tile to tile.  Two CTAs per SM cover each other's chains; K / V rings of three tiles keep about 100 KB per CTA
+// sums, and the digits of w = s_v 2^(x - u) for the second product (per-head modes: w = p, without s_v), 2^u the row's
+// largest weight so far, halved until it is less than twice the tile's own largest: w is at most 1 whatever the scales'
+// range, and the digits' fixed step stays small beside a tile's weights, however far these lie below the row's
+// largest (a long history's many small weights would otherwise count in the row sum alone).  O is kept in registers,
+// rescaled from tile to tile, by whole powers of two while the maximum stays.  Two CTAs per SM cover each other's chains; K / V rings of three tiles keep about 100 KB per CTA
 // in flight.  Work is shared out as paged_sched.cuh says; a CTA's rings run on across its items.
 // Measured (combine included): 16 sequences of up to 32768 tokens, 32 / 8 heads of 128, int8 per head (760 MB): 127 to
 // 130 us, 5.8 to 6.0 TB/s, 89 to 91 % of the copy bandwidth (with warp-level 16-bit MMAs on converted codes: 221), fp8 per token
@@ -34,7 +34,7 @@ using namespace paged;
 constexpr int TK = 128;     // keys per tile
 constexpr int NST = 3;      // K / V stages
 constexpr int DT = 192;     // warp 0 loads, warp 1 MMAs, warps 2-5 softmax
-// How far (powers of two) a tile's unit may lie below the largest: fp32 holds O in the lower one, and what 2^24 below it is
+// How far (powers of two) a tile's unit may lie below the largest weight: fp32 holds O in the lower one, and what 2^24 below it is
 // lost weighs 2^-84 of the largest weight.
 constexpr float kFall = 60.0f;
 
@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(DT, 2)
     do {
       const Seq s = run.it.s;
       const int hk = run.it.hk, b = run.it.b, rows = s.m * p.G;
-      // o is in units of 2^unit (l too, in the per-head modes); top: the largest unit that a tile has had.  Lane r of every
+      // o is in units of 2^(top - down) (l too, in the per-head modes), top the running maximum, down whole.  Lane r of every
       // warp keeps row r's; in the per-token modes lane R + r does, and lane r the maximum of x, which is l's unit.
-      float unit = -INFINITY, top = -INFINITY;
+      float top = -INFINITY, down = 0.0f;
       const bool unit_lane = !TOK || lane >= R;
       float l_run[R], o[R];
 #pragma unroll
@@ -446,14 +446,16 @@ __global__ void __launch_bounds__(DT, 2)
         }
         uint8_t* sp = smem + L::P + (L::NP == 2 ? bb : 0) * N * 128;
         if (lane < JOBS) {
-          // the tile's unit: the largest weight of its keys as a power of two, but not kFall below the largest so far
+          // the tile's unit: the largest weight so far, or the last of its halves that is not below the tile's own largest
           const float* rd = red + bb * 4 * JOBS + lane;
-          float c = fmaxf(fmaxf(fmaxf(rd[0], rd[JOBS]), fmaxf(rd[2 * JOBS], rd[3 * JOBS])), -INFINITY);
-          if (unit_lane) c = ceilf(c);
-          top = fmaxf(top, c);
-          const float un = unit_lane ? fmaxf(c, top - kFall) : top, base = un == -INFINITY ? 0.0f : un;
-          const float al = attn::ex2(unit - base);  // of a unit: a whole power; 0 from -inf
-          unit = un;
+          const float c = fmaxf(fmaxf(fmaxf(rd[0], rd[JOBS]), fmaxf(rd[2 * JOBS], rd[3 * JOBS])), -INFINITY);
+          const float mx_new = fmaxf(top, c);
+          const float d = unit_lane ? fminf(floorf(mx_new - c), kFall) : 0.0f;
+          const bool none = mx_new == -INFINITY;
+          const float base = none ? 0.0f : mx_new - d;
+          const float al = none ? 0.0f : attn::ex2((top - mx_new) + (d - down));  // a whole power while the maximum stays; 0 from -inf
+          top = mx_new;
+          down = d;
           if (unit_lane) alb[(bb * 4 + wg) * R + lane % R] = al;
           reinterpret_cast<float2*>(units + wg * R + lane % R)[TOK && !unit_lane] = make_float2(base, al);
         }
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(DT, 2)
       // (mv, o's factor) and, in the per-token modes, (m, 1): o and the per-head l in units of 2^mv
       if (lane < JOBS)
         reinterpret_cast<float2*>(units + wg * R + lane % R)[TOK && !unit_lane] =
-            make_float2(top, top == -INFINITY ? 1.0f : attn::ex2(unit - top));
+            make_float2(top, top == -INFINITY ? 1.0f : attn::ex2(-down));
       __syncwarp();
       const bool whole = run.u == run.it.first && run.it.first + run.it.nt <= run.u1;
       const int slot = 2 * blockIdx.x + (run.u == run.u0 ? 0 : 1);

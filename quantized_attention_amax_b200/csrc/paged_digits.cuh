@@ -3,7 +3,7 @@
 // the codes).  Three MMA columns then stand for one row, and the products add up in 32 bits:
 //   int8 caches:  v = d2 2^16 + d1 2^8 + d0, signed digits, for a query row scaled by a power of two so that
 //                 |v| < 2^22: bf16 values down to 2^-14 of the row's largest are exact, smaller ones are
-//                 off by at most 2^-22 of it.  Probabilities, held against a power of two over the largest of their
+//                 off by at most 2^-22 of it.  Probabilities, held against a unit below twice the largest of their
 //                 key tile, are 24-bit integers, unsigned digits.
 //   E4M3 caches:  v = t1 + t2 / 16 + t3 / 256, each digit the E4M3 rounding of 16 times what the digits
 //                 before leave: |v| < 256, relative error 2^-12, and 2^-18 absolute (2^-25 of the row's, or the key

@@ -512,8 +512,8 @@ FAQ_API fa_status fa_paged_evict(const fa_paged_cache* cache, const fa_paged_bat
 /* Synchronise `s`, read and clear this device's status word.  Returns
  * FA_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
  * FA_ERR_BOUNDS if an index check failed (the paged operators' checks of
- * lengths, pages and positions; every other index in a library built with
- * FA_DEBUG_BOUNDS) -- the access was skipped, so the outputs are not valid --,
+ * lengths, pages and positions; the other computed global indices in a library
+ * built with FA_DEBUG_BOUNDS) -- the access was skipped, so the outputs are not valid --,
  * FA_ERR_CUDA if the stream reports an error, FA_OK otherwise.  The first
  * event since the last check is the one reported. */
 FAQ_API fa_status fa_check_device_status(fa_stream_t s);

@@ -17,7 +17,7 @@
 // the largest of them, whatever the scales' range: w_j = s_v(j) 2^(x_j - mv), mv the running maximum of
 // x + log2 s_v, and the sum of p is that of 2^(x_j - mv).
 // Work is shared out as paged_sched.cuh says: a causal block counts the key tiles it sees.
-// Measured: two chunks of up to 1500 tokens behind up to 32768, 32 / 8 heads of 128: int8 per head 1.57 ms (829 TFLOP/s,
+// Measured: two chunks of up to 1500 tokens behind up to 32768, 32 / 8 heads of 128: int8 per head 1.60 ms (810 TFLOP/s,
 // 50 % of the library GEMM's rate), fp8 per head 1.58, fp8 per token 3.06 ms (426 TFLOP/s; 11.2 ms with warp-level MMAs).
 // Per head, a step of both tiles takes about 4000 cycles where the exponentials alone take 2048: the chain from one
 // product through a softmax to the next.  Per token the softmax is the longer side (3100 to 4500 cycles): both scales of

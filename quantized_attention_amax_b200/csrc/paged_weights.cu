@@ -11,8 +11,8 @@
 // tiles in turn (64 rows of one tile at a time each), so one's MMAs run under the other's exponentials.
 // Units are 128 keys of one (sequence, kv head); the CTAs take equal runs of them, counted from the lengths on
 // the device.
-// Measured: one token to each of 16 sequences of up to 16384 (int8 per head, 212 MB): 48 us, 4.4 TB/s; 64 tokens to two of
-// up to 32768 (fp8 per token): 103 us, the exponentials' loops of eight warps (four warpgroups with 32 rows a step
+// Measured: one token to each of 16 sequences of up to 16384 (int8 per head, 212 MB): 47 us, 4.5 TB/s; 64 tokens to two of
+// up to 32768 (fp8 per token): 101 us, the exponentials' loops of eight warps (four warpgroups with 32 rows a step
 // spill registers and take as long, with 16 rows a step 142 us).
 #include "paged_digits.cuh"
 #include "paged_sched.cuh"

@@ -8,9 +8,9 @@
 // codes pass once.  A warp takes one token and a run of its heads, so the token's sequence, position
 // and angles are found once (its first rows are on their way meanwhile); each lane holds 8 elements (16 bytes)
 // of a row, D / 8 lanes a row, and the (i, i + rotary_dim / 2) pairs meet by shuffles.
-// Measured: 32768 tokens of 32 query and 8 kv heads of 128 (int8 per token, 757 MB) in 164 us, 4.6 TB/s, 70 % of
-// the copy bandwidth (what is left: a warp waits for two rows at a time, and more in flight costs more in registers
-// than it brings); 16 tokens in 6.3 us, a launch and four dependent loads.
+// Measured: 32768 tokens of 32 query and 8 kv heads of 128 (int8 per token, 757 MB) in 165 us, 4.6 TB/s, 70 % of
+// the copy bandwidth (what is left: 74 % of the issue slots are taken by unpacking, rotating and quantizing, and more rows
+// in flight cost more in registers than they bring); 16 tokens in 6.5 us, a launch and four dependent loads.
 #include <cuda_bf16.h>
 
 #include "paged_common.cuh"

@@ -152,13 +152,15 @@ def empty_paged_cache(pages: int, H: int, page_size: int, D: int, mode: str, lay
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None) -> Tuple[list, float]:
     """The pairs' rotation frequencies f_i = base^(-2 i / rotary_dim), scaled for long contexts, and
     the factor on cos and sin.  ``scaling`` is None or a dict with "type" and
-      "linear": f_i / factor;
+      "linear": f_i / factor (S. Chen, S. Wong, L. Chen and Y. Tian, "Extending Context Window of Large
+                Language Models via Positional Interpolation", 2023);
       "ntk":    the base times factor^(rotary_dim / (rotary_dim - 2)), so the slowest pair slows by
                 ``factor`` and the fastest stays;
       "yarn":   f_i / factor for pairs that turn less than ``beta_slow`` (1) times in ``original``
                 positions, f_i for those that turn more than ``beta_fast`` (32) times, between them a
                 linear blend over the pair index; cos and sin times 0.1 ln(factor) + 1 (or
-                ``attention_factor``);
+                ``attention_factor``) (B. Peng, J. Quesnelle, H. Fan and E. Shippole, "YaRN: Efficient
+                Context Window Extension of Large Language Models", 2023);
       "bands":  f_i / factor for wavelengths over original / ``low`` (1), f_i below original / ``high``
                 (4), between them a blend linear in original / wavelength.
     Host arithmetic in 64 bits."""
@@ -256,7 +258,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, causa
                     softmax_scale: float = 0.0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                     return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
     """Attention of the new tokens q [T, Hq, D] over the cache (fa_paged_attention), bf16 [T, Hq, D].
-    Returns out, or (out, lse) with return_lse (lse fp32 [T, Hq]).  ``workspace``: bytes to use where it is
+    q, out, lse and the workspace must not overlap.  Returns out, or (out, lse) with return_lse (lse fp32 [T, Hq]).  ``workspace``: bytes to use where it is
     large enough (paged_attention_workspace_size), else it is allocated."""
     tq = _rows(q, "q")
     ref = ctypes.byref
@@ -283,7 +285,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, causa
 def paged_weights(q: torch.Tensor, lse: torch.Tensor, cache: PagedCache, batch: PagedBatch, acc: torch.Tensor,
                   causal: bool = True, softmax_scale: float = 0.0, accumulate: bool = True) -> torch.Tensor:
     """Add to acc (fp32 [B, Hkv, n]) the attention weight the new tokens give each cached token, or
-    with accumulate=False set it (fa_paged_weights).  ``lse`` as paged_attention returned it."""
+    with accumulate=False set it (fa_paged_weights).  ``lse`` as paged_attention returned it; rows where it
+    is not finite give nothing."""
     tq = _rows(q, "q")
     ref = ctypes.byref
     if acc.dim() != 3 or tuple(acc.shape[:2]) != (batch.B, cache.H):

@@ -419,7 +419,7 @@ FAQ_API fa_status fa_rope_table(float* table, int positions, int rotary_dim, con
  *   overlap q, k or v otherwise (columns of one matrix side by side do not;
  *   ranges that cross at two strides count as overlapping: FA_ERR_INVALID_ARG).
  *   Both NULL: K and V only.  A page written by this call must not be another
- *   sequence's page too.
+ *   sequence's page too, nor stand twice in its own.
  */
 FAQ_API fa_status fa_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_paged_cache* cache,
                                  const fa_paged_batch* batch, const float* cos_sin, int table_positions,
@@ -502,7 +502,8 @@ FAQ_API fa_status fa_paged_weights(const fa_rows* q, const float* lse, const fa_
  *   order, then 0.  The outputs must not overlap each other, scores, seq_lens
  *   or page_table (FA_ERR_INVALID_ARG).  batch->cu_q is not used.  Keys
  *   keep the rotation of their first positions, so later tokens need explicit
- *   positions in fa_rope_append.  A page must not be in two sequences.
+ *   positions in fa_rope_append.  A page must not be in two sequences, nor
+ *   twice in one.
  *   budget: 1 to 2^30 (above: FA_ERR_UNSUPPORTED); sink + recent <= budget.
  */
 FAQ_API fa_status fa_paged_evict(const fa_paged_cache* cache, const fa_paged_batch* batch, const float* scores,

@@ -351,7 +351,7 @@ FAQ_API size_t fa_attention_workspace_size_qkv(const fa_qtensor* q, const fa_qte
  * FA_MODE_FP8_PER_HEAD (scales fp32 [H]), FA_MODE_INT8_PER_TOKEN or
  * FA_MODE_FP8_PER_TOKEN (scales fp32 [pages, H, page_size] in either layout);
  * others -> FA_ERR_UNSUPPORTED (a scale over several tokens, or packed codes,
- * would have to be requantized by an append).
+ * would have to be requantized by an append).  Scales are not negative.
  * codes: one byte each, [pages, H, page_size, D] (BNSD) or
  * [pages, page_size, H, D] (BSND), 16-byte aligned.  D: 64 or 128.
  * pages: at least 1.  page_size: a power of two from 16 to 1024. */
